@@ -67,7 +67,7 @@ def lib() -> ctypes.CDLL:
     import torch  # noqa: F401
     L = ctypes.CDLL(LIB_PATH)
     vp, pp, sz, i32 = ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p), ctypes.c_size_t, ctypes.c_int
-    i64p = ctypes.POINTER(ctypes.c_int64)
+    i64p, f32 = ctypes.POINTER(ctypes.c_int64), ctypes.c_float
     sig = {
         "coll_allreduce": [pp, pp, i32, sz, i32, i32, vp],
         "coll_allreduce_algo": [pp, pp, i32, sz, i32, i32, i32, vp],
@@ -92,6 +92,17 @@ def lib() -> ctypes.CDLL:
         "coll_moe_dispatch": [pp, pp, pp, pp, vp, vp, i32, sz, i32, sz, i64p, i32, vp],
         "coll_moe_dispatch_fp8": [pp, pp, pp, pp, vp, vp, vp, i32, sz, i32, sz, sz, i64p, vp],
         "coll_moe_combine_direct": [pp, pp, pp, pp, pp, i32, sz, i32, sz, i64p, i32, vp],
+        "coll_layernorm": [pp, pp, pp, pp, pp, pp, i32, sz, sz, f32, i32, i32, vp],
+        "coll_layernorm_ckpt8": [pp, pp, pp, pp, pp, pp, pp, i32, sz, sz, sz, f32, i32, i32, vp],
+        "coll_layernorm_backward": [pp, pp, pp, pp, pp, pp, pp, pp, i32, sz, sz, i32, i32, i32, vp, sz, vp],
+        "coll_layernorm_backward_ckpt8": [pp, pp, pp, pp, pp, pp, pp, pp, pp, pp, i32, sz, sz, sz, i32, i32, i32, vp,
+                                          sz, vp],
+        "coll_ckpt8_save": [pp, pp, i32, sz, sz, sz, i32, vp],
+        "coll_ckpt8_load": [pp, pp, i32, sz, sz, sz, i32, vp],
+        "coll_swiglu_ckpt8": [pp, pp, pp, i32, sz, sz, sz, i32, vp],
+        "coll_swiglu_backward_ckpt8": [pp, pp, pp, pp, i32, sz, sz, sz, i32, vp],
+        "coll_vocab_logprob": [pp, i64p, i64p, vp, f32, pp, pp, pp, i32, pp, pp, i32, sz, i32, vp, sz, vp],
+        "coll_vocab_logprob_backward": [pp, i64p, i64p, vp, f32, vp, vp, vp, vp, pp, i64p, i32, sz, i32, vp],
         "coll_stream_probe": [pp, i32, pp, i32, sz, i32, ctypes.c_uint, vp, vp],
     }
     for name, args in sig.items():
@@ -106,6 +117,12 @@ def lib() -> ctypes.CDLL:
     L.coll_version.restype = ctypes.c_int
     L.coll_moe_fp8_row_bytes.argtypes = [sz, sz]
     L.coll_moe_fp8_row_bytes.restype = sz
+    L.coll_layernorm_workspace_bytes.argtypes = [i32, sz, sz]
+    L.coll_layernorm_workspace_bytes.restype = sz
+    L.coll_ckpt8_row_bytes.argtypes = [sz, sz]
+    L.coll_ckpt8_row_bytes.restype = sz
+    L.coll_vocab_logprob_workspace_bytes.argtypes = [i32, sz, i64p, i32]
+    L.coll_vocab_logprob_workspace_bytes.restype = sz
     L.coll_finalize.argtypes = []
     L.coll_finalize.restype = None
     L.coll_set_grid_limit.argtypes = [ctypes.c_int]
@@ -622,6 +639,307 @@ def coll_allreduce_batch(calls: Sequence[tuple], p: int, flags: int = 0, stream=
         arr[k].n, arr[k].dtype, arr[k].op = int(n), int(dtype), int(op)
     fname = "coll_allreduce_batch_noalloc" if noalloc else "coll_allreduce_batch"
     return _run(fname, (arr, len(calls), int(p), int(flags), _stream(stream)), fname, defer, (arr, keep))
+
+
+# ----------------------------------------------------------------------------
+# Token-wise operators of a training step
+# ----------------------------------------------------------------------------
+
+def _opt_array(xs):
+    return _ptr_array(xs) if xs is not None else (None, None)
+
+
+def _same_ranks(p: int, *lists) -> None:
+    for xs in lists:
+        if xs is not None and len(xs) != p:
+            raise ValueError("every argument must list the same ranks")
+
+
+def _f32(what: str, *lists) -> None:
+    import torch
+    for xs in lists:
+        for x in xs or []:
+            if hasattr(x, "dtype") and x.dtype != torch.float32:
+                raise ValueError(f"{what} must be float32")
+
+
+def _wdtype_of(lists, wdtype: int | None, dt: int) -> int:
+    """The weights' type: given, or that of the first weight listed, else dt."""
+    have = [xs for xs in lists if xs is not None]
+    if wdtype is None:
+        wdtype = _dtype_of(have[0][0], None) if have and hasattr(have[0][0], "dtype") else dt
+    for xs in have:
+        _same_dtype(xs, wdtype)
+    return int(wdtype)
+
+
+def _rows_of(x, hidden: int, rows: int | None) -> int:
+    return int(rows) if rows is not None else _numel(x, None) // int(hidden)
+
+
+def _layernorm(fname, x, gamma, beta, y, mean, rstd, ckpt, hidden, group, eps, rows, dtype, wdtype, stream, defer):
+    p = len(x)
+    _same_ranks(p, gamma, beta, y, mean, rstd, ckpt)
+    dt = _dtype_of(x[0], dtype)
+    _same_dtype([*x, *y], dt)
+    wt = _wdtype_of([gamma, beta], wdtype, dt)
+    rows = _rows_of(x[0], hidden, rows)
+    _check_sizes([*x, *y], rows * hidden, fname)
+    _check_sizes([*(gamma or []), *(beta or [])], hidden, fname + " weights")
+    _check_sizes([*(mean or []), *(rstd or [])], rows, fname + " mean/rstd")
+    _f32(fname + " mean/rstd", mean, rstd)
+    arrays = [_ptr_array(x), _opt_array(gamma), _opt_array(beta), _ptr_array(y), _opt_array(mean), _opt_array(rstd)]
+    tail = (p, rows, int(hidden))
+    if ckpt is not None:
+        _check_sizes(ckpt, rows * coll_ckpt8_row_bytes(hidden, group), fname + " ckpt")
+        arrays.append(_ptr_array(ckpt))
+        tail += (int(group),)
+    return _run(fname, (*[a for a, _ in arrays], *tail, float(eps), dt, wt, _stream(stream)), fname, defer,
+                tuple(k for _, k in arrays))
+
+
+def coll_layernorm(x, gamma, beta, y, hidden: int, eps: float = 1e-5, mean=None, rstd=None, rows: int | None = None,
+                   dtype: int | None = None, wdtype: int | None = None, stream=None, defer: bool = False):
+    """Layer norm of each rank's rows [rows*hidden]; gamma and beta (or
+    None) list every rank's copy; mean and rstd (or None) fp32 [rows]."""
+    return _layernorm("coll_layernorm", x, gamma, beta, y, mean, rstd, None, hidden, 0, eps, rows, dtype, wdtype,
+                      stream, defer)
+
+
+def coll_layernorm_ckpt8(x, gamma, beta, y, mean, rstd, ckpt, hidden: int, group: int, eps: float = 1e-5,
+                         rows: int | None = None, dtype: int | None = None, wdtype: int | None = None, stream=None,
+                         defer: bool = False):
+    """coll_layernorm that also keeps x in 8 bits: ckpt uint8
+    [rows * coll_ckpt8_row_bytes(hidden, group)]."""
+    if ckpt is None:
+        raise ValueError("ckpt lists the checkpoint buffers")
+    return _layernorm("coll_layernorm_ckpt8", x, gamma, beta, y, mean, rstd, ckpt, hidden, group, eps, rows, dtype,
+                      wdtype, stream, defer)
+
+
+def coll_layernorm_workspace_bytes(p: int, rows: int, hidden: int) -> int:
+    return int(lib().coll_layernorm_workspace_bytes(int(p), int(rows), int(hidden)))
+
+
+def _workspace(ws, nbytes: int | None):
+    if nbytes is None:
+        nbytes = ws.numel() * ws.element_size() if hasattr(ws, "numel") else None
+    if nbytes is None:
+        raise ValueError("workspace_bytes must be given for raw addresses")
+    return _addr(ws), int(nbytes)
+
+
+def _layernorm_backward(fname, dy, x, mean, rstd, gamma, beta, dx, y, dgamma, dbeta, workspace, hidden, group, op, rows,
+                        dtype, wdtype, workspace_bytes, stream, defer):
+    p = len(dy)
+    _same_ranks(p, x, mean, rstd, gamma, beta, dx, y, dgamma, dbeta)
+    dt = _dtype_of(dy[0], dtype)
+    _same_dtype([*dy, *dx, *(y or [])], dt)
+    wt = _wdtype_of([gamma, beta, dgamma, dbeta], wdtype, dt)
+    rows = _rows_of(dy[0], hidden, rows)
+    _check_sizes([*dy, *dx, *(y or [])], rows * hidden, fname)
+    _check_sizes([w for ws in (gamma, beta, dgamma, dbeta) for w in ws or []], hidden, fname + " weights")
+    _check_sizes([*mean, *rstd], rows, fname + " mean/rstd")
+    _f32(fname + " mean/rstd", mean, rstd)
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    from_ckpt = group is not None
+    if from_ckpt:
+        _check_sizes(x, rows * coll_ckpt8_row_bytes(hidden, group), fname + " ckpt")
+        arrays = [_ptr_array(dy), _ptr_array(x), _ptr_array(mean), _ptr_array(rstd), _opt_array(gamma),
+                  _opt_array(beta), _ptr_array(dx), _opt_array(y), _opt_array(dgamma), _opt_array(dbeta)]
+        shape = (p, rows, int(hidden), int(group))
+    else:
+        _same_dtype(x, dt)
+        _check_sizes(x, rows * hidden, fname)
+        arrays = [_ptr_array(dy), _ptr_array(x), _ptr_array(mean), _ptr_array(rstd), _opt_array(gamma),
+                  _ptr_array(dx), _opt_array(dgamma), _opt_array(dbeta)]
+        shape = (p, rows, int(hidden))
+    return _run(fname, (*[a for a, _ in arrays], *shape, int(op), dt, wt, ws, nbytes, _stream(stream)), fname, defer,
+                (*[k for _, k in arrays], workspace))
+
+
+def coll_layernorm_backward(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, workspace, hidden: int, op: int = COLL_SUM,
+                            rows: int | None = None, dtype: int | None = None, wdtype: int | None = None,
+                            workspace_bytes: int | None = None, stream=None, defer: bool = False):
+    """dx of each rank's rows; dgamma and dbeta (or None), summed or averaged
+    (op) over all rows of all ranks, go to every rank.  workspace: a device
+    buffer of coll_layernorm_workspace_bytes(p, rows, hidden)."""
+    return _layernorm_backward("coll_layernorm_backward", dy, x, mean, rstd, gamma, None, dx, None, dgamma, dbeta,
+                               workspace, hidden, None, op, rows, dtype, wdtype, workspace_bytes, stream, defer)
+
+
+def coll_layernorm_backward_ckpt8(dy, ckpt, mean, rstd, gamma, dx, dgamma, dbeta, workspace, hidden: int, group: int,
+                                  op: int = COLL_SUM, beta=None, y=None, rows: int | None = None,
+                                  dtype: int | None = None, wdtype: int | None = None,
+                                  workspace_bytes: int | None = None, stream=None, defer: bool = False):
+    """coll_layernorm_backward from the 8-bit checkpoint of x; y (or None)
+    gets the forward's output again (beta is only needed for it)."""
+    return _layernorm_backward("coll_layernorm_backward_ckpt8", dy, ckpt, mean, rstd, gamma, beta, dx, y, dgamma, dbeta,
+                               workspace, hidden, int(group), op, rows, dtype, wdtype, workspace_bytes, stream, defer)
+
+
+def coll_ckpt8_row_bytes(hidden: int, group: int) -> int:
+    """Bytes of one checkpoint row; 0 if the shape is not accepted."""
+    return int(lib().coll_ckpt8_row_bytes(int(hidden), int(group)))
+
+
+def _ckpt8(fname, first, second, rows_list, ckpt, hidden, group, rows, dtype, stream, defer):
+    p = len(first)
+    _same_ranks(p, second)
+    dt = _dtype_of(rows_list[0], dtype)
+    _same_dtype(rows_list, dt)
+    rows = _rows_of(rows_list[0], hidden, rows)
+    _check_sizes(rows_list, rows * hidden, fname)
+    _check_sizes(ckpt, rows * coll_ckpt8_row_bytes(hidden, group), fname + " ckpt")
+    a, k1 = _ptr_array(first)
+    b, k2 = _ptr_array(second)
+    return _run(fname, (a, b, p, rows, int(hidden), int(group), dt, _stream(stream)), fname, defer, (k1, k2))
+
+
+def coll_ckpt8_save(x, ckpt, hidden: int, group: int, rows: int | None = None, dtype: int | None = None, stream=None,
+                    defer: bool = False):
+    """Rows [rows*hidden] to 8-bit checkpoints, uint8 [rows * row_bytes]."""
+    return _ckpt8("coll_ckpt8_save", x, ckpt, x, ckpt, hidden, group, rows, dtype, stream, defer)
+
+
+def coll_ckpt8_load(ckpt, x, hidden: int, group: int, rows: int | None = None, dtype: int | None = None, stream=None,
+                    defer: bool = False):
+    """The rows that 8-bit checkpoints hold."""
+    return _ckpt8("coll_ckpt8_load", ckpt, x, x, ckpt, hidden, group, rows, dtype, stream, defer)
+
+
+def coll_swiglu_ckpt8(gate_up, out, ckpt, ffn: int, group: int, rows: int | None = None, dtype: int | None = None,
+                      stream=None, defer: bool = False):
+    """out = silu(gate) * up of rows [gate | up] (2*ffn elements), which ckpt
+    keeps in 8 bits: uint8 [rows * coll_ckpt8_row_bytes(2 * ffn, group)]."""
+    p = len(gate_up)
+    _same_ranks(p, out, ckpt)
+    dt = _dtype_of(gate_up[0], dtype)
+    _same_dtype([*gate_up, *out], dt)
+    rows = _rows_of(gate_up[0], 2 * ffn, rows)
+    _check_sizes(gate_up, rows * 2 * ffn, "coll_swiglu_ckpt8 gate_up")
+    _check_sizes(out, rows * ffn, "coll_swiglu_ckpt8 out")
+    _check_sizes(ckpt, rows * coll_ckpt8_row_bytes(2 * ffn, group), "coll_swiglu_ckpt8 ckpt")
+    arrays = [_ptr_array(gate_up), _ptr_array(out), _ptr_array(ckpt)]
+    return _run("coll_swiglu_ckpt8", (*[a for a, _ in arrays], p, rows, int(ffn), int(group), dt, _stream(stream)),
+                "coll_swiglu_ckpt8", defer, tuple(k for _, k in arrays))
+
+
+def coll_swiglu_backward_ckpt8(ckpt, dout, dgate_up, ffn: int, group: int, out=None, rows: int | None = None,
+                               dtype: int | None = None, stream=None, defer: bool = False):
+    """The gradient of [gate | up] from its 8-bit checkpoint; out (or None)
+    gets the forward's output again."""
+    p = len(dout)
+    _same_ranks(p, ckpt, dgate_up, out)
+    dt = _dtype_of(dout[0], dtype)
+    _same_dtype([*dout, *dgate_up, *(out or [])], dt)
+    rows = _rows_of(dout[0], ffn, rows)
+    _check_sizes(dgate_up, rows * 2 * ffn, "coll_swiglu_backward_ckpt8 dgate_up")
+    _check_sizes([*dout, *(out or [])], rows * ffn, "coll_swiglu_backward_ckpt8 dout/out")
+    _check_sizes(ckpt, rows * coll_ckpt8_row_bytes(2 * ffn, group), "coll_swiglu_backward_ckpt8 ckpt")
+    arrays = [_ptr_array(ckpt), _ptr_array(dout), _ptr_array(dgate_up), _opt_array(out)]
+    return _run("coll_swiglu_backward_ckpt8", (*[a for a, _ in arrays], p, rows, int(ffn), int(group), dt,
+                                               _stream(stream)), "coll_swiglu_backward_ckpt8", defer,
+                tuple(k for _, k in arrays))
+
+
+def _i64_array(vals):
+    return (ctypes.c_int64 * len(vals))(*[int(v) for v in vals])
+
+
+def _shard_array(xs, rows: int, vocab, ld, what: str):
+    """Pointers, sizes and row strides of vocabulary shards: 2-d tensors
+    [rows, vocab] whose rows are contiguous (column slices included), or raw
+    addresses with vocab and ld given."""
+    ptrs, vs, lds = [], [], []
+    for i, x in enumerate(xs):
+        if isinstance(x, int):
+            if vocab is None or ld is None:
+                raise ValueError(f"{what}: vocab and ld must be given for raw addresses")
+            ptrs.append(x)
+            vs.append(int(vocab[i]))
+            lds.append(int(ld[i]))
+            continue
+        if not x.is_cuda:
+            raise ValueError("buffers must be device tensors")
+        if x.dim() != 2 or x.shape[0] < rows or (x.shape[1] > 1 and x.stride(1) != 1):
+            raise ValueError(f"{what}: shards must be [rows, vocab] with contiguous rows")
+        v = int(x.shape[1]) if vocab is None else int(vocab[i])
+        if v > x.shape[1]:
+            raise ValueError(f"{what}: shard of {x.shape[1]} entries, {v} needed")
+        ptrs.append(x.data_ptr())
+        vs.append(v)
+        lds.append(max(int(x.stride(0)), v) if x.shape[0] <= 1 else int(x.stride(0)))
+    arr, keep = _ptr_array(ptrs)
+    return arr, _i64_array(vs), _i64_array(lds), keep
+
+
+def _targets(targets, rows: int | None):
+    import torch
+    if hasattr(targets, "dtype") and targets.dtype != torch.int64:
+        raise ValueError("targets must be a device int64 tensor")
+    return _numel(targets, rows)
+
+
+def coll_vocab_logprob_workspace_bytes(rows: int, vocab: Sequence[int], top_k: int = 0) -> int:
+    """Workspace of coll_vocab_logprob; vocab lists every rank's shard."""
+    return int(lib().coll_vocab_logprob_workspace_bytes(len(vocab), int(rows), _i64_array(vocab), int(top_k)))
+
+
+def coll_vocab_logprob(logits, targets, stats, logp, workspace, entropy=None, top_k: int = 0, top_logp=None,
+                       top_idx=None, inv_temp: float = 1.0, vocab: Sequence[int] | None = None,
+                       ld: Sequence[int] | None = None, rows: int | None = None, dtype: int | None = None,
+                       workspace_bytes: int | None = None, stream=None, defer: bool = False):
+    """Log probabilities of targets (device int64 [rows]) over the shards
+    logits[r] [rows, vocab_r]; every rank gets stats fp32 [rows, 2], logp and
+    entropy (or None) fp32 [rows], top_logp fp32 and top_idx int32
+    [rows, top_k]."""
+    import torch
+    p = len(logits)
+    _same_ranks(p, stats, logp, entropy, top_logp, top_idx)
+    rows = _targets(targets, rows)
+    dt = _dtype_of(logits[0], dtype)
+    _same_dtype(logits, dt)
+    z, v, l, k0 = _shard_array(logits, rows, vocab, ld, "vocab_logprob logits")
+    _check_sizes(stats, 2 * rows, "vocab_logprob stats")
+    _check_sizes([*logp, *(entropy or [])], rows, "vocab_logprob logp/entropy")
+    _f32("vocab_logprob results", stats, logp, entropy, top_logp)
+    if top_k:
+        if top_logp is None or top_idx is None:
+            raise ValueError("top_k needs top_logp and top_idx")
+        _check_sizes([*top_logp, *top_idx], rows * top_k, "vocab_logprob top")
+        if any(hasattr(x, "dtype") and x.dtype != torch.int32 for x in top_idx):
+            raise ValueError("top_idx must be int32")
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    arrays = [_ptr_array(stats), _ptr_array(logp), _opt_array(entropy)]
+    tops = [_opt_array(top_logp if top_k else None), _opt_array(top_idx if top_k else None)]
+    return _run("coll_vocab_logprob", (z, l, v, _addr(targets), float(inv_temp), *[a for a, _ in arrays], int(top_k),
+                                       *[a for a, _ in tops], p, rows, dt, ws, nbytes, _stream(stream)),
+                "coll_vocab_logprob", defer, (k0, v, l, *[k for _, k in arrays + tops], workspace))
+
+
+def coll_vocab_logprob_backward(logits, targets, stats, dlogp, dlogits, entropy=None, dentropy=None,
+                                inv_temp: float = 1.0, vocab: Sequence[int] | None = None,
+                                ld: Sequence[int] | None = None, dld: Sequence[int] | None = None,
+                                rows: int | None = None, dtype: int | None = None, stream=None, defer: bool = False):
+    """Gradient of the logits from one rank's stats (and entropy) of the
+    forward pass and the gradients of logp and (or None) of the entropy."""
+    p = len(logits)
+    _same_ranks(p, dlogits)
+    rows = _targets(targets, rows)
+    dt = _dtype_of(logits[0], dtype)
+    _same_dtype([*logits, *dlogits], dt)
+    z, v, l, k0 = _shard_array(logits, rows, vocab, ld, "vocab_logprob_backward logits")
+    dz, dv, dl, k1 = _shard_array(dlogits, rows, list(v), dld, "vocab_logprob_backward dlogits")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs the forward pass's entropy")
+    _check_sizes([stats], 2 * rows, "vocab_logprob_backward stats")
+    _check_sizes([x for x in (dlogp, entropy, dentropy) if x is not None], rows, "vocab_logprob_backward gradients")
+    _f32("vocab_logprob_backward stats and gradients", [x for x in (stats, dlogp, entropy, dentropy) if x is not None])
+    opt = lambda x: _addr(x) if x is not None else None  # noqa: E731
+    return _run("coll_vocab_logprob_backward", (z, l, v, _addr(targets), float(inv_temp), _addr(stats), _addr(dlogp),
+                                                opt(entropy), opt(dentropy), dz, dl, p, rows, dt, _stream(stream)),
+                "coll_vocab_logprob_backward", defer, (k0, k1, v, l, dl))
 
 
 def coll_status_string(status: int) -> str:

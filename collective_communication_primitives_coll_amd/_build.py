@@ -33,6 +33,9 @@ SOURCES = [
     "batch_kernels.hip",
     "moe_kernels.hip",
     "fp8_kernels.hip",
+    "layernorm_kernels.hip",
+    "ckpt8_kernels.hip",
+    "logprob_kernels.hip",
     "probe_kernels.hip",
     "batch_noalloc.hip",
     "claim_slots.hip",

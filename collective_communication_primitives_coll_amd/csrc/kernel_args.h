@@ -166,6 +166,104 @@ struct Fp8Args {
   int p;
 };
 
+// Token-wise operators.  A launch takes up to kArgRanks ranks (the rank is
+// the grid's second dimension), so that its pointer arrays stay well below
+// the 4 KiB of a kernel's arguments; more ranks take a second launch.
+constexpr int kArgRanks = 32;
+
+struct LnArgs {
+  const void* x[kArgRanks];      // rows; backward from a checkpoint: its rows
+  const void* dy[kArgRanks];     // backward
+  const void* gamma[kArgRanks];  // or null: ones
+  const void* beta[kArgRanks];   // or null: zeros
+  float* mean[kArgRanks];        // forward: written unless null; backward: read
+  float* rstd[kArgRanks];
+  void* y[kArgRanks];            // backward from a checkpoint: or null
+  void* dx[kArgRanks];
+  uint8_t* ckpt[kArgRanks];      // forward with a checkpoint
+  float* ws;                     // backward: partial sums [p][groups][2][hidden]
+  uint64_t rows;                 // per rank
+  uint64_t hidden;
+  uint64_t row_bytes;            // of a checkpoint row
+  uint32_t gsh;                  // log2 of a checkpoint group's units of 8
+  int rank0;                     // the launch's first rank
+  float eps;
+};
+
+struct LnJoinArgs {
+  void* dgamma[kMaxRanks];       // null where absent
+  void* dbeta[kMaxRanks];
+  const float* ws;               // [parts][2][hidden]
+  uint64_t hidden;
+  uint32_t parts;
+  int p;
+  int avg;
+};
+
+// 8-bit checkpoints and the gated activation.
+enum Ckpt8Kind : int { kCkpt8Save = 0, kCkpt8Load = 1, kSwigluForward = 2, kSwigluBackward = 3 };
+struct Ckpt8Args {
+  const void* src[kArgRanks];    // rows; backward: dout
+  void* dst[kArgRanks];          // load: rows; forward: out; backward: the rows' gradient
+  void* again[kArgRanks];        // backward: the output again, or null
+  uint8_t* ckpt[kArgRanks];
+  uint64_t rows;
+  uint64_t hidden;               // elements of a checkpoint row
+  uint64_t units;                // units of 8 that a lane's walk counts per row
+  uint64_t row_bytes;
+  uint64_t div_mul;              // division by units (set by the launcher)
+  uint32_t div_shift;
+  uint32_t gsh;
+};
+// Units of a row stay below this, so that a row's unit and a tile's offset
+// past it keep to 31 bits.
+constexpr uint64_t kCkpt8MaxUnits = uint64_t{1} << 30;
+
+// Vocabulary log probabilities over p shards.  A row's shard is cut into
+// segs[rank] pieces; all pieces of a row number at most kMaxPieces (a wave).
+constexpr int kMaxPieces = 64;
+constexpr int kMaxTop = 32;
+struct LogprobPlan {
+  int pieces;                    // per row, over all ranks
+  int first[kMaxRanks + 1];      // first piece of each rank, and the end
+  int64_t len[kMaxRanks];        // elements per piece (the rank's last may be shorter)
+};
+struct LogprobArgs {
+  const void* logits[kMaxRanks];
+  int64_t ld[kMaxRanks];         // elements from row to row
+  int64_t first_index[kMaxRanks + 1];  // first vocabulary index of each shard, and the end
+  LogprobPlan plan;
+  const int64_t* targets;
+  float* part;                   // [rows][pieces][4]: max, sum, entropy sum, target's logit (-inf where elsewhere)
+  unsigned long long* keys;      // [rows][pieces][top]
+  uint64_t rows;
+  float scale;                   // inverse temperature
+  int p;
+  int top;
+};
+struct LogprobJoinArgs {
+  float* stats[kMaxRanks];       // [rows][2]
+  float* logp[kMaxRanks];
+  float* entropy[kMaxRanks];     // null where absent
+  float* top_logp[kMaxRanks];    // [rows][top]
+  int32_t* top_idx[kMaxRanks];
+};
+struct LogprobGradArgs {
+  const void* logits[kMaxRanks];
+  void* dlogits[kMaxRanks];
+  int64_t ld[kMaxRanks];
+  int64_t dld[kMaxRanks];
+  int64_t first_index[kMaxRanks + 1];
+  const int64_t* targets;
+  const float* stats;            // [rows][2]
+  const float* dlogp;
+  const float* entropy;          // null without dentropy
+  const float* dentropy;
+  uint64_t rows;
+  float scale;
+  int p;
+};
+
 // Literal ring: one neighbour step per launch.
 struct RingStepGeom {
   uint64_t n;
@@ -257,6 +355,23 @@ int launch_moe_dequant_fp8(const Fp8Args& a, int max_grid, void* stream);
 int launch_moe_dispatch(int elem_bytes, const MoeDirectArgs& a, int max_grid, void* stream);
 int launch_moe_dispatch_fp8(const MoeDirectArgs& a, int max_grid, void* stream);
 int launch_moe_combine_direct(int dtype, const MoeRowArgs& a, int max_grid, void* stream);
+
+// Layer norm.  Workgroups per rank of each pass (the backward pass's also
+// fixes its workspace and so depends on the shape alone).
+uint32_t ln_forward_groups(int ranks, int tpr);
+uint32_t ln_backward_groups(int p, uint64_t rows, uint64_t hidden);
+int launch_ln_forward(int dtype, int wdtype, const LnArgs& a, int ranks, bool ckpt, void* stream);
+int launch_ln_backward(int dtype, int wdtype, const LnArgs& a, int ranks, uint32_t groups, bool ckpt, void* stream);
+int launch_ln_join(int wdtype, const LnJoinArgs& a, void* stream);
+
+// 8-bit checkpoints and the gated activation (kind: Ckpt8Kind).
+int launch_ckpt8(int kind, int dtype, Ckpt8Args a, int ranks, void* stream);
+
+// Vocabulary log probabilities: the pieces' pass and the join over them,
+// then the logits' gradient.
+void logprob_plan(int p, uint64_t rows, const int64_t* vocab, LogprobPlan* plan);
+int launch_logprob(int dtype, const LogprobArgs& a, const LogprobJoinArgs& j, void* stream);
+int launch_logprob_backward(int dtype, const LogprobGradArgs& a, void* stream);
 
 // Direction-mix bandwidth probe: ns source and nd destination streams of
 // nvec 16-byte vectors each, `unroll` vectors per lane per tile

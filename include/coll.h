@@ -422,6 +422,144 @@ coll_status_t coll_allreduce_batch(const coll_call_t* calls, int ncalls, int p,
 coll_status_t coll_allreduce_batch_noalloc(const coll_call_t* calls, int ncalls, int p, unsigned flags,
                                            void* stream);
 
+/* ===========================================================================
+ * Token-wise operators of a training step
+ *
+ * What a data- or tensor-parallel training step computes between its
+ * collectives and its matrix products, over the same p logical ranks and
+ * under the same contract: host arrays of p device pointers, everything
+ * validated before anything is enqueued, nothing allocated (the caller
+ * owns the workspaces), asynchronous on `stream`.  Rank arrays documented
+ * as optional may be NULL as a whole.  Statistics and sums are fp32; bf16
+ * results are narrowed once.  dtype: COLL_F32 or COLL_BF16 (COLL_I32
+ * returns COLL_ERR_UNSUPPORTED).  Results are the same from run to run and
+ * do not depend on coll_set_grid_limit.
+ * ======================================================================== */
+
+/* Layer norm, forward.  x[r]: `rows` rows of `hidden` elements, row after
+ * row; for every row
+ *   m = mean x,  s = 1 / sqrt(mean (x - m)^2 + eps),
+ *   y = (x - m) s gamma + beta.
+ * gamma[r], beta[r]: rank r's copy of the weights, `hidden` elements of
+ * type wdtype (COLL_F32, or dtype); optional (ones, zeros).
+ * mean[r], rstd[r]: fp32 [rows], m and s for the backward pass; optional.
+ * In place: y[r] == x[r].  1 <= hidden < 2^31; rows == 0 is a no-op. */
+coll_status_t coll_layernorm(const void* const* x, const void* const* gamma, const void* const* beta, void* const* y,
+                             float* const* mean, float* const* rstd, int p, size_t rows, size_t hidden, float eps,
+                             coll_dtype_t dtype, coll_dtype_t wdtype, void* stream);
+
+/* Layer norm, backward, with data parallelism's AllReduce of the weights'
+ * gradients.  With n = (x - m) s and w = dy gamma, per row
+ *   dx = s (w - mean w - n mean(w n)),
+ * and over all rows of all ranks
+ *   dgamma = sum dy n,  dbeta = sum dy,
+ * divided by p for COLL_AVG; op is COLL_SUM or COLL_AVG (others
+ * COLL_ERR_UNSUPPORTED).  Every rank gets the total: dgamma[r], dbeta[r]
+ * hold `hidden` elements of wdtype, each array optional.  mean and rstd are
+ * those of the forward pass.  workspace: device memory of at least
+ * coll_layernorm_workspace_bytes(p, rows, hidden) bytes, 16-byte aligned.
+ * In place: dx[r] == dy[r].  rows == 0 writes zeros to dgamma and dbeta. */
+coll_status_t coll_layernorm_backward(const void* const* dy, const void* const* x, const float* const* mean,
+                                      const float* const* rstd, const void* const* gamma, void* const* dx,
+                                      void* const* dgamma, void* const* dbeta, int p, size_t rows, size_t hidden,
+                                      coll_op_t op, coll_dtype_t dtype, coll_dtype_t wdtype, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Workspace of the backward pass; 0 if the shape is not accepted. */
+size_t coll_layernorm_workspace_bytes(int p, size_t rows, size_t hidden);
+
+/* Activation checkpoints in 8 bits.  A row of `hidden` elements becomes
+ * coll_ckpt8_row_bytes(hidden, group) bytes in the format of
+ * coll_moe_pack_fp8: e4m3 codes, one fp32 scale per `group` elements, zero
+ * padding (a row received from the FP8 dispatch is such a checkpoint).
+ * Each element comes back as code * scale, within 2^-4 of its value or
+ * 2^-10 of its group's scale.  A group that holds a NaN or an infinity
+ * comes back as NaN throughout, so that an overflow stays visible.
+ * group: a power of two from 16 to 512 that divides hidden (else
+ * COLL_ERR_UNSUPPORTED, or COLL_ERR_INVALID_ARG where it does not divide).
+ * Checkpoint buffers are 16-byte aligned and hold `rows` packed rows; no
+ * in-place forms; rows == 0 is a no-op. */
+size_t coll_ckpt8_row_bytes(size_t hidden, size_t group);
+coll_status_t coll_ckpt8_save(const void* const* x, void* const* ckpt, int p, size_t rows, size_t hidden, size_t group,
+                              coll_dtype_t dtype, void* stream);
+coll_status_t coll_ckpt8_load(const void* const* ckpt, void* const* x, int p, size_t rows, size_t hidden, size_t group,
+                              coll_dtype_t dtype, void* stream);
+
+/* Layer norm that also keeps its input in 8 bits (ckpt[r]), and the
+ * backward pass from that checkpoint: as coll_layernorm and
+ * coll_layernorm_backward with x replaced by what the checkpoint holds
+ * (mean and rstd stay those of the exact rows).  y (optional): the
+ * forward's output computed again from the checkpoint, n gamma + beta
+ * (beta optional), for the weight gradient of the product it fed. */
+coll_status_t coll_layernorm_ckpt8(const void* const* x, const void* const* gamma, const void* const* beta,
+                                   void* const* y, float* const* mean, float* const* rstd, void* const* ckpt, int p,
+                                   size_t rows, size_t hidden, size_t group, float eps, coll_dtype_t dtype,
+                                   coll_dtype_t wdtype, void* stream);
+coll_status_t coll_layernorm_backward_ckpt8(const void* const* dy, const void* const* ckpt, const float* const* mean,
+                                            const float* const* rstd, const void* const* gamma,
+                                            const void* const* beta, void* const* dx, void* const* y,
+                                            void* const* dgamma, void* const* dbeta, int p, size_t rows,
+                                            size_t hidden, size_t group, coll_op_t op, coll_dtype_t dtype,
+                                            coll_dtype_t wdtype, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/* Gated activation with its input kept in 8 bits.  gate_up[r]: rows of
+ * 2 * ffn elements, the gate g then the linear part u;
+ *   out = g u / (1 + e^-g)       (rows of ffn elements)
+ * and ckpt[r] gets the rows of 2 * ffn elements.  group divides ffn.
+ * Backward, with g and u as the checkpoint holds them and
+ * s = 1 / (1 + e^-g):
+ *   dgate_up = [dout u s (1 + g (1 - s)) | dout g s],
+ * and out (optional) the forward's output from the checkpoint, for the
+ * weight gradient of the product it fed.  ffn < 2^30. */
+coll_status_t coll_swiglu_ckpt8(const void* const* gate_up, void* const* out, void* const* ckpt, int p, size_t rows,
+                                size_t ffn, size_t group, coll_dtype_t dtype, void* stream);
+coll_status_t coll_swiglu_backward_ckpt8(const void* const* ckpt, const void* const* dout, void* const* dgate_up,
+                                         void* const* out, int p, size_t rows, size_t ffn, size_t group,
+                                         coll_dtype_t dtype, void* stream);
+
+/* Log probabilities over a sharded vocabulary (tensor parallelism: rank r
+ * holds the logits of vocab[r] consecutive entries; the maximum and the sum
+ * over all shards take the place of two AllReduces).
+ *   logits[r]   rows of vocab[r] elements, ld[r] elements from row to row
+ *               (ld, vocab: HOST int64[p]; vocab[r] may be 0; at most
+ *               2^31 - 1 entries in all, indexed rank after rank);
+ *   targets     device int64 [rows]: the given tokens, one copy for all
+ *               ranks; a target outside the vocabulary (padding) counts as
+ *               absent: its logp is 0 and has no gradient.
+ * With t = inv_temp (finite, > 0), m a row's largest logit, every rank gets
+ *   stats[r]    fp32 [rows][2]: m and L = log sum_j exp((z_j - m) t), so that
+ *               log p_j = (z_j - m) t - L;
+ *   logp[r]     fp32 [rows]: log p of the target;
+ *   entropy[r]  fp32 [rows]: -sum p_j log p_j (optional);
+ *   top_logp[r], top_idx[r]  fp32 and int32 [rows][top_k], 0 <= top_k <= 32:
+ *               the likeliest entries by descending logit, ties to the lower
+ *               index; where the vocabulary ends first, -inf and -1.
+ * Logits of -infinity are masked entries (probability 0).  A row with
+ * nothing else: m = L = logp = -inf, entropy 0, gradient 0.  A row that holds
+ * a NaN or +infinity: NaN throughout, alternatives -1.
+ * workspace: coll_vocab_logprob_workspace_bytes(p, rows, vocab, top_k)
+ * bytes, 16-byte aligned.  rows == 0 is a no-op. */
+coll_status_t coll_vocab_logprob(const void* const* logits, const int64_t* ld, const int64_t* vocab,
+                                 const int64_t* targets, float inv_temp, float* const* stats, float* const* logp,
+                                 float* const* entropy, int top_k, float* const* top_logp, int32_t* const* top_idx,
+                                 int p, size_t rows, coll_dtype_t dtype, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+size_t coll_vocab_logprob_workspace_bytes(int p, size_t rows, const int64_t* vocab, int top_k);
+
+/* The logits' gradient: stats (and entropy, with dentropy) are one rank's
+ * results of the forward pass, dlogp and dentropy (optional) fp32 [rows] the
+ * gradients of logp and of the entropy;
+ *   dlogits_j = t (dlogp (1[j = target] - p_j) - dentropy p_j (log p_j + H)),
+ * written to rank r's shard with dld[r] elements from row to row (shards may
+ * be column slices of one matrix).  In place: dlogits[r] == logits[r] with
+ * dld[r] == ld[r]. */
+coll_status_t coll_vocab_logprob_backward(const void* const* logits, const int64_t* ld, const int64_t* vocab,
+                                          const int64_t* targets, float inv_temp, const float* stats,
+                                          const float* dlogp, const float* entropy, const float* dentropy,
+                                          void* const* dlogits, const int64_t* dld, int p, size_t rows,
+                                          coll_dtype_t dtype, void* stream);
+
 /* Direction-mix bandwidth probe: a measurement helper, not a collective.
  * [A] 4.1 models a collective's time by the bandwidth of each resource it
  * uses, and [A] 2.5 compares bus bandwidth with what the hardware

@@ -1,0 +1,195 @@
+"""Host-side checks of the token-wise operators' entry points: refusals,
+workspaces, overlaps and empty calls, none of which reaches the device."""
+import ctypes
+
+import pytest
+
+import collective_communication_primitives_coll_amd as coll
+from test_abi_cpu import _arr, host_only
+
+OK, INV, UNS, AL = coll.COLL_OK, coll.COLL_ERR_INVALID_ARG, coll.COLL_ERR_UNSUPPORTED, coll.COLL_ERR_ALIAS
+F32, BF16, I32, U8 = 0, 1, 2, 3
+BASE = 0x7F0000000000
+P = 4
+
+
+class Bufs:
+    """Made-up rank arrays, far apart."""
+
+    def __init__(self):
+        self.keep, self.next = [], BASE
+
+    def __call__(self, off=0, p=P, step=0x10000000):
+        a, k = _arr([self.next + off + step * r for r in range(p)])
+        self.next += step * (p + 1)
+        self.keep.append(k)
+        return a
+
+    def one(self, off=0):
+        self.next += 0x10000000
+        return self.next - 0x10000000 + off
+
+
+def _i64(*v):
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+def test_shape_functions():
+    rb = coll.coll_ckpt8_row_bytes
+    assert rb(7168, 128) == 7168 + 56 * 4 and rb(16, 16) == 32 and rb(512, 512) == 528
+    for hidden, group in [(0, 16), (100, 16), (64, 0), (64, 8), (96, 48), (1024, 1024), (1 << 31, 512)]:
+        assert rb(hidden, group) == 0, (hidden, group)
+    ws = coll.coll_layernorm_workspace_bytes
+    assert ws(0, 10, 64) == 0 and ws(65, 10, 64) == 0 and ws(4, 10, 0) == 0 and ws(4, 1 << 60, 64) == 0
+    for p, rows, hidden in [(1, 1, 1), (8, 4096, 7168), (64, 3, 100), (3, 5, 40000)]:
+        n = ws(p, rows, hidden)
+        assert n > 0 and n % (p * 2 * hidden * 4) == 0
+    lw = coll.coll_vocab_logprob_workspace_bytes
+    assert lw(0, [100], 4) == 0 and lw(4, [100] * 65, 4) == 0 and lw(4, [-1, 5], 4) == 0 and lw(4, [10], 33) == 0
+    for rows, vocab, top in [(1, [1], 0), (3, [50257], 32), (5, [0, 9, 0], 1), (2048, [16384] * 8, 8), (7, [1000] * 64, 5)]:
+        n = lw(rows, vocab, top)
+        per = 16 + 8 * top
+        assert n > 0 and n % (rows * per) == 0 and n // (rows * per) <= 64
+
+
+def test_no_rows_is_ok_without_pointers():
+    L = coll.lib()
+    assert L.coll_layernorm(None, None, None, None, None, None, P, 0, 64, 1e-5, BF16, BF16, None) == OK
+    assert L.coll_layernorm_ckpt8(None, None, None, None, None, None, None, P, 0, 64, 16, 1e-5, BF16, F32, None) == OK
+    assert L.coll_layernorm_backward(None, None, None, None, None, None, None, None, P, 0, 64, 0, F32, F32, None, 0, None) == OK
+    assert L.coll_ckpt8_save(None, None, P, 0, 64, 32, F32, None) == OK
+    assert L.coll_ckpt8_load(None, None, P, 0, 64, 32, F32, None) == OK
+    assert L.coll_swiglu_ckpt8(None, None, None, P, 0, 64, 32, BF16, None) == OK
+    assert L.coll_swiglu_backward_ckpt8(None, None, None, None, P, 0, 64, 32, BF16, None) == OK
+    ld = _i64(8, 8, 8, 8)
+    assert L.coll_vocab_logprob(None, ld, ld, None, 1.0, None, None, None, 0, None, None, P, 0, F32, None, 0, None) == OK
+    assert L.coll_vocab_logprob_backward(None, ld, ld, None, 1.0, None, None, None, None, None, ld, P, 0, F32, None) == OK
+
+
+@host_only
+def test_layernorm_refusals():
+    L = coll.lib()
+    b = Bufs()
+    x, g, be, y, m, s, ck = b(), b(), b(), b(), b(), b(), b()
+    odd, hole, holek = b(off=1), *_arr([BASE, 0, BASE + 64, BASE + 128])
+
+    def fwd(x=x, g=g, be=be, y=y, m=m, s=s, p=P, rows=10, hidden=64, eps=1e-5, dt=BF16, wt=BF16):
+        return L.coll_layernorm(x, g, be, y, m, s, p, rows, hidden, eps, dt, wt, None)
+    assert fwd(p=0) == INV and fwd(p=65) == INV and fwd(hidden=0) == INV and fwd(dt=U8) == INV and fwd(dt=7) == INV
+    assert fwd(dt=I32, wt=I32) == UNS and fwd(dt=F32, wt=BF16) == UNS and fwd(wt=I32) == UNS and fwd(hidden=1 << 31) == UNS
+    assert fwd(rows=1 << 60) == INV and fwd(eps=-1.0) == INV and fwd(eps=float("nan")) == INV and fwd(eps=float("inf")) == INV
+    assert fwd(x=None) == INV and fwd(y=None) == INV and fwd(x=hole) == INV and fwd(g=hole) == INV and fwd(m=hole) == INV
+    assert fwd(x=odd) == INV and fwd(y=odd) == INV and fwd(g=odd) == INV and fwd(s=odd) == INV
+    assert fwd(y=g) == AL and fwd(m=s) == AL and fwd(m=x) == AL and fwd(y=m) == AL
+    near, _k = _arr([x[r] + 64 for r in range(P)])       # the output half over its input
+    assert fwd(y=near) == AL
+    swap, _k2 = _arr([x[1], x[0], x[2], x[3]])           # another rank's input
+    assert fwd(y=swap) == AL
+
+    def ckpt(ck=ck, group=16, hidden=64, m=m):
+        return L.coll_layernorm_ckpt8(x, g, be, y, m, s, ck, P, 10, hidden, group, 1e-5, BF16, BF16, None)
+    assert ckpt(ck=None) == INV and ckpt(ck=hole) == INV and ckpt(ck=b(off=8)) == INV and ckpt(group=0) == INV
+    assert ckpt(group=48, hidden=96) == UNS and ckpt(group=1024, hidden=1024) == UNS and ckpt(hidden=72) == INV
+    assert ckpt(ck=y) == AL and ckpt(ck=x) == AL
+
+    dy, dx, dg, db, ws = b(), b(), b(), b(), b.one()
+    need = coll.coll_layernorm_workspace_bytes(P, 10, 64)
+
+    def bwd(dy=dy, x=x, m=m, s=s, g=g, dx=dx, dg=dg, db=db, op=0, ws=ws, n=need, wt=BF16, rows=10):
+        return L.coll_layernorm_backward(dy, x, m, s, g, dx, dg, db, P, rows, 64, op, BF16, wt, ws, n, None)
+    assert bwd(op=1) == UNS and bwd(op=2) == UNS and bwd(op=9) == INV and bwd(ws=None) == INV and bwd(n=need - 1) == INV
+    assert bwd(ws=ws + 4) == INV and bwd(dy=None) == INV and bwd(m=None) == INV and bwd(s=hole) == INV and bwd(dg=hole) == INV
+    assert bwd(dx=odd) == INV and bwd(db=odd) == INV
+    assert bwd(dx=x) == AL and bwd(dg=db) == AL and bwd(dg=g) == AL and bwd(ws=dx[0]) == AL and bwd(dx=m) == AL
+    assert bwd(rows=0, dg=db) == AL
+
+    def bck(y=None, be=None, group=16, x=ck):
+        return L.coll_layernorm_backward_ckpt8(dy, x, m, s, g, be, dx, y, dg, db, P, 10, 64, group, 0, BF16, BF16, ws, need, None)
+    assert bck(group=24) == INV and bck(group=8) == UNS and bck(y=hole) == INV and bck(y=dx) == AL and bck(y=ck) == AL
+    assert bck(x=b(off=2)) == INV and bck(be=odd) == INV
+
+
+@host_only
+def test_checkpoint_and_gated_activation_refusals():
+    L = coll.lib()
+    b = Bufs()
+    x, ck, out, dx = b(), b(), b(), b()
+    odd = b(off=1)
+    for f in (lambda a, c, **k: L.coll_ckpt8_save(a, c, k.get("p", P), k.get("rows", 9), k.get("h", 64), k.get("g", 32), k.get("dt", BF16), None),
+              lambda a, c, **k: L.coll_ckpt8_load(c, a, k.get("p", P), k.get("rows", 9), k.get("h", 64), k.get("g", 32), k.get("dt", BF16), None)):
+        assert f(x, ck, p=0) == INV and f(x, ck, h=65) == INV and f(x, ck, g=8) == UNS and f(x, ck, h=96, g=48) == UNS
+        assert f(x, ck, dt=I32) == UNS and f(x, ck, dt=U8) == INV and f(None, ck) == INV and f(x, None) == INV
+        assert f(odd, ck) == INV and f(x, odd) == INV and f(x, x) == AL and f(x, ck, rows=1 << 59) == INV
+
+    def fwd(x=x, out=out, ck=ck, ffn=64, g=32, dt=BF16, p=P):
+        return L.coll_swiglu_ckpt8(x, out, ck, p, 9, ffn, g, dt, None)
+    assert fwd(p=65) == INV and fwd(ffn=0) == INV and fwd(ffn=48) == INV and fwd(g=16, ffn=1 << 30) == UNS and fwd(dt=I32) == UNS
+    assert fwd(out=None) == INV and fwd(ck=odd) == INV and fwd(out=x) == AL and fwd(ck=out) == AL and fwd(g=1024, ffn=1024) == UNS
+
+    dout, dgu = b(), b()
+
+    def bwd(ck=ck, dout=dout, dgu=dgu, out=None, ffn=64, g=32):
+        return L.coll_swiglu_backward_ckpt8(ck, dout, dgu, out, P, 9, ffn, g, BF16, None)
+    assert bwd(ck=None) == INV and bwd(dout=odd) == INV and bwd(out=odd) == INV and bwd(g=0) == INV
+    assert bwd(dgu=dout) == AL and bwd(dgu=ck) == AL and bwd(out=dout) == AL and bwd(out=dgu) == AL
+
+
+@host_only
+def test_logprob_refusals():
+    L = coll.lib()
+    b = Bufs()
+    z, st, lp, en, tl, ti, dz = b(), b(), b(), b(), b(), b(), b()
+    t, ws = b.one(), b.one()
+    vocab, ld = _i64(100, 100, 100, 50), _i64(100, 100, 128, 50)
+    need = coll.coll_vocab_logprob_workspace_bytes(9, list(vocab), 4)
+
+    def fwd(z=z, ld=ld, vocab=vocab, t=t, temp=1.0, st=st, lp=lp, en=en, k=4, tl=tl, ti=ti, p=P, dt=BF16, ws=ws, n=need, rows=9):
+        return L.coll_vocab_logprob(z, ld, vocab, t, temp, st, lp, en, k, tl, ti, p, rows, dt, ws, n, None)
+    assert fwd(p=0) == INV and fwd(p=65) == INV and fwd(dt=U8) == INV and fwd(dt=I32) == UNS and fwd(k=-1) == INV and fwd(k=33) == UNS
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        assert fwd(temp=bad) == INV
+    assert fwd(ld=None) == INV and fwd(vocab=None) == INV and fwd(ld=_i64(99, 100, 100, 50)) == INV
+    assert fwd(vocab=_i64(-1, 2, 2, 2)) == INV and fwd(vocab=_i64(0, 0, 0, 0)) == INV
+    big = _i64(1 << 30, 1 << 30, 1 << 30, 1 << 30)
+    assert fwd(vocab=big, ld=big) == UNS
+    assert fwd(t=None) == INV and fwd(t=t + 4) == INV and fwd(st=None) == INV and fwd(lp=None) == INV and fwd(tl=None) == INV
+    assert fwd(z=None) == INV and fwd(z=b(off=1)) == INV and fwd(en=b(off=2)) == INV
+    assert fwd(ws=None) == INV and fwd(n=need - 1) == INV and fwd(ws=ws + 8) == INV
+    assert fwd(st=lp) == AL and fwd(st=z) == AL and fwd(ws=z[0]) == AL and fwd(tl=ti) == AL and fwd(lp=en) == AL
+    assert fwd(t=st[0]) == AL
+
+    s1, d1, e1, h1 = b.one(), b.one(), b.one(), b.one()
+
+    def bwd(z=z, dz=dz, dld=ld, st=s1, dlp=d1, en=e1, den=h1, t=t, ld=ld, temp=1.0):
+        return L.coll_vocab_logprob_backward(z, ld, vocab, t, temp, st, dlp, en, den, dz, dld, P, 9, BF16, None)
+    assert bwd(temp=0.0) == INV and bwd(dz=None) == INV and bwd(dld=None) == INV and bwd(dld=_i64(100, 100, 99, 50)) == INV
+    assert bwd(st=None) == INV and bwd(dlp=None) == INV and bwd(en=None) == INV and bwd(den=h1 + 1) == INV
+    assert bwd(st=dz[1]) == AL and bwd(t=dz[3]) == AL and bwd(den=dz[0]) == AL
+    assert bwd(dz=z, dld=_i64(104, 100, 128, 50)) == AL               # in place, but another stride
+    cross, _k = _arr([z[1], z[0], dz[2], dz[3]])
+    assert bwd(dz=cross) == AL
+    same, _k2 = _arr([dz[0], dz[0], dz[2], dz[3]])
+    assert bwd(dz=same) == AL
+    # column slices of one matrix may stand side by side, not across each other
+    lds = _i64(350, 350, 350, 350)
+    cols, _k3 = _arr([dz[0] + 2 * c for c in (0, 90, 200, 300)])      # the first two share ten columns
+    assert bwd(dz=cols, dld=lds, z=z) == AL
+    wrap, _k4 = _arr([dz[0] + 2 * c for c in (0, 100, 200, 320)])     # the last runs into the next row's first
+    assert bwd(dz=wrap, dld=lds) == AL
+
+
+def test_binding_refuses_before_the_call():
+    import torch
+    z = torch.zeros(2, 3)
+    with pytest.raises(ValueError):
+        coll.coll_vocab_logprob([z], torch.zeros(2, dtype=torch.int64), [z], [z], z)        # host tensors
+    with pytest.raises(ValueError):
+        coll.coll_vocab_logprob([z], torch.zeros(2, dtype=torch.int32), [z], [z], z)        # int32 targets
+    with pytest.raises(ValueError):
+        coll.coll_layernorm([1, 2], None, None, [1], 8, rows=1, dtype=F32)                  # unlike rank counts
+    with pytest.raises(ValueError):
+        coll.coll_layernorm_ckpt8([1], None, None, [1], None, None, None, 16, 16, rows=1, dtype=F32)
+    with pytest.raises(ValueError):
+        coll.coll_vocab_logprob_backward([1], 1, 1, 1, [1], rows=1, dtype=F32)              # raw addresses, no sizes
+    with pytest.raises(ValueError):
+        coll.coll_layernorm_backward([1], [1], [1], [1], None, [1], None, None, 1, 8, rows=1, dtype=F32)  # no workspace size
