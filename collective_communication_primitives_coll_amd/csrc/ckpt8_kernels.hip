@@ -9,7 +9,7 @@
 //
 // Bound by HBM: forward moves 8 bytes an element pair in bf16 (4 + 2 + 2),
 // backward 10 with the output written again, at about 30 fp32 operations.
-// The rows are cut into units of 8 elements that the lanes take in their
+// The rows are cut into units of 16 bytes that the lanes take in their
 // order through the whole rank, rows one after the other, so narrow rows
 // leave no lanes idle.  A group is whole units, its first unit at a
 // multiple of the group's lane count, so it lies within one wave and its
@@ -64,116 +64,116 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f));
 }
 
-template <int DT>
+template <int DT, int E>
 __global__ __launch_bounds__(kBlock) void ckpt8_save_kernel(Ckpt8Args a) {
   const int rank = blockIdx.y;
   struct State {
-    RawUnit<DT> x;
+    RawUnit<DT, E> x;
   };
   walk_units<State>(
       a,
-      [&](State& s, uint64_t row, uint32_t u, bool in) {
-        s.x = in ? load_unit<DT, true>(static_cast<const uint8_t*>(a.src[rank]) + row * a.hidden * Traits<DT>::B, u)
-                 : zero_unit<DT>();
+      [&](State& s, uint64_t row, uint64_t u, bool in) {
+        s.x = in ? load_unit<DT, E, true>(static_cast<const uint8_t*>(a.src[rank]) + row * a.hidden * Traits<DT>::B, u * E)
+                 : zero_unit<DT, E>();
       },
-      [&](State& s, uint64_t row, uint32_t u, bool in) {
-        float f[8];
+      [&](State& s, uint64_t row, uint64_t u, bool in) {
+        float f[E];
         widen_unit(s.x, f);
-        const RawUnit<kE4M3> q = encode_unit<DT>(s.x, f, a.gsh);
-        if (in) store_codes<true>(a.ckpt[rank] + row * a.row_bytes, a.hidden, a.row_bytes, u, a.gsh, q);
+        const RawUnit<kE4M3, E> q = encode_unit<DT, E>(s.x, f, a.glog);
+        if (in) store_codes<E, true>(a.ckpt[rank] + row * a.row_bytes, a.hidden, a.row_bytes, u * E, a.glog, q);
       });
 }
 
-template <int DT>
+template <int DT, int E>
 __global__ __launch_bounds__(kBlock) void ckpt8_load_kernel(Ckpt8Args a) {
   const int rank = blockIdx.y;
   struct State {
-    RawUnit<kE4M3> q;
+    RawUnit<kE4M3, E> q;
   };
   walk_units<State>(
       a,
-      [&](State& s, uint64_t row, uint32_t u, bool in) {
-        s.q = in ? load_codes<true>(a.ckpt[rank] + row * a.row_bytes, a.hidden, u, a.gsh) : zero_unit<kE4M3>();
+      [&](State& s, uint64_t row, uint64_t u, bool in) {
+        s.q = in ? load_codes<E, true>(a.ckpt[rank] + row * a.row_bytes, a.hidden, u * E, a.glog) : zero_unit<kE4M3, E>();
       },
-      [&](State& s, uint64_t row, uint32_t u, bool in) {
-        float f[8];
+      [&](State& s, uint64_t row, uint64_t u, bool in) {
+        float f[E];
         widen_unit(s.q, f);
-        if (in) store_unit<DT, true>(static_cast<uint8_t*>(a.dst[rank]) + row * a.hidden * Traits<DT>::B, u, narrow_unit<DT>(f));
+        if (in) store_unit<DT, E, true>(static_cast<uint8_t*>(a.dst[rank]) + row * a.hidden * Traits<DT>::B, u * E, narrow_unit<DT, E>(f));
       });
 }
 
-// a.hidden: elements of a checkpoint row, 2 * ffn; a.units: units of ffn.
-template <int DT>
+// a.hidden: elements of a checkpoint row, 2 * ffn; a.width: ffn.
+template <int DT, int E>
 __global__ __launch_bounds__(kBlock) void swiglu_forward_kernel(Ckpt8Args a) {
   const int rank = blockIdx.y;
   struct State {
-    RawUnit<DT> g, u;
+    RawUnit<DT, E> g, u;
   };
   walk_units<State>(
       a,
-      [&](State& s, uint64_t row, uint32_t j, bool in) {
+      [&](State& s, uint64_t row, uint64_t j, bool in) {
         if (in) {
           const uint8_t* x = static_cast<const uint8_t*>(a.src[rank]) + row * a.hidden * Traits<DT>::B;
-          s.g = load_unit<DT, true>(x, j);
-          s.u = load_unit<DT, true>(x, a.units + j);
+          s.g = load_unit<DT, E, true>(x, j * E);
+          s.u = load_unit<DT, E, true>(x, (a.units + j) * E);
         } else {
-          s.g = s.u = zero_unit<DT>();
+          s.g = s.u = zero_unit<DT, E>();
         }
       },
-      [&](State& s, uint64_t row, uint32_t j, bool in) {
-        float g[8], u[8];
+      [&](State& s, uint64_t row, uint64_t j, bool in) {
+        float g[E], u[E];
         widen_unit(s.g, g);
         widen_unit(s.u, u);
-        const RawUnit<kE4M3> qg = encode_unit<DT>(s.g, g, a.gsh), qu = encode_unit<DT>(s.u, u, a.gsh);
+        const RawUnit<kE4M3, E> qg = encode_unit<DT, E>(s.g, g, a.glog), qu = encode_unit<DT, E>(s.u, u, a.glog);
         if (!in) return;
         uint8_t* c = a.ckpt[rank] + row * a.row_bytes;
-        store_codes<true>(c, a.hidden, a.row_bytes, j, a.gsh, qg);
-        store_codes<true>(c, a.hidden, a.row_bytes, a.units + j, a.gsh, qu);
+        store_codes<E, true>(c, a.hidden, a.row_bytes, j * E, a.glog, qg);
+        store_codes<E, true>(c, a.hidden, a.row_bytes, (a.units + j) * E, a.glog, qu);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) u[e] *= g[e] * sigmoid(g[e]);
-        store_unit<DT, true>(static_cast<uint8_t*>(a.dst[rank]) + row * (a.hidden / 2) * Traits<DT>::B, j, narrow_unit<DT>(u));
+        for (int e = 0; e < E; ++e) u[e] *= g[e] * sigmoid(g[e]);
+        store_unit<DT, E, true>(static_cast<uint8_t*>(a.dst[rank]) + row * (a.hidden / 2) * Traits<DT>::B, j * E, narrow_unit<DT, E>(u));
       });
 }
 
-template <int DT>
+template <int DT, int E>
 __global__ __launch_bounds__(kBlock) void swiglu_backward_kernel(Ckpt8Args a) {
   const int rank = blockIdx.y;
   struct State {
-    RawUnit<kE4M3> g, u;
-    RawUnit<DT> dy;
+    RawUnit<kE4M3, E> g, u;
+    RawUnit<DT, E> dy;
   };
   walk_units<State>(
       a,
-      [&](State& s, uint64_t row, uint32_t j, bool in) {
+      [&](State& s, uint64_t row, uint64_t j, bool in) {
         if (in) {
           const uint8_t* c = a.ckpt[rank] + row * a.row_bytes;
-          s.g = load_codes<true>(c, a.hidden, j, a.gsh);
-          s.u = load_codes<true>(c, a.hidden, a.units + j, a.gsh);
-          s.dy = load_unit<DT, true>(static_cast<const uint8_t*>(a.src[rank]) + row * (a.hidden / 2) * Traits<DT>::B, j);
+          s.g = load_codes<E, true>(c, a.hidden, j * E, a.glog);
+          s.u = load_codes<E, true>(c, a.hidden, (a.units + j) * E, a.glog);
+          s.dy = load_unit<DT, E, true>(static_cast<const uint8_t*>(a.src[rank]) + row * (a.hidden / 2) * Traits<DT>::B, j * E);
         } else {
-          s.g = s.u = zero_unit<kE4M3>();
-          s.dy = zero_unit<DT>();
+          s.g = s.u = zero_unit<kE4M3, E>();
+          s.dy = zero_unit<DT, E>();
         }
       },
-      [&](State& s, uint64_t row, uint32_t j, bool in) {
+      [&](State& s, uint64_t row, uint64_t j, bool in) {
         if (!in) return;
-        float g[8], u[8], dy[8];
+        float g[E], u[E], dy[E];
         widen_unit(s.g, g);
         widen_unit(s.u, u);
         widen_unit(s.dy, dy);
-        float again[8];
+        float again[E];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < E; ++e) {
           const float sg = sigmoid(g[e]), act = g[e] * sg;
           again[e] = act * u[e];
           g[e] = dy[e] * u[e] * sg * (1.0f + g[e] * (1.0f - sg));
           u[e] = dy[e] * act;
         }
         uint8_t* dx = static_cast<uint8_t*>(a.dst[rank]) + row * a.hidden * Traits<DT>::B;
-        store_unit<DT, true>(dx, j, narrow_unit<DT>(g));
-        store_unit<DT, true>(dx, a.units + j, narrow_unit<DT>(u));
+        store_unit<DT, E, true>(dx, j * E, narrow_unit<DT, E>(g));
+        store_unit<DT, E, true>(dx, (a.units + j) * E, narrow_unit<DT, E>(u));
         if (a.again[rank])
-          store_unit<DT, true>(static_cast<uint8_t*>(a.again[rank]) + row * (a.hidden / 2) * Traits<DT>::B, j, narrow_unit<DT>(again));
+          store_unit<DT, E, true>(static_cast<uint8_t*>(a.again[rank]) + row * (a.hidden / 2) * Traits<DT>::B, j * E, narrow_unit<DT, E>(again));
       });
 }
 
@@ -181,8 +181,12 @@ __global__ __launch_bounds__(kBlock) void swiglu_backward_kernel(Ckpt8Args a) {
 
 int launch_ckpt8(int kind, int dtype, Ckpt8Args a, int ranks, void* stream) {
   hipStream_t s = (hipStream_t)stream;
+  // 16-byte units; a group of 512 in fp32 would span two waves of them, and
+  // takes units of 8 elements
+  const int elems = dtype == kF32 && a.glog < 9 ? 4 : 8;
+  a.units = a.width / elems;
   // exact division by the units of a row, for the 31-bit values of
-  // row_index: with 2^sh >= d, m = ceil(2^(31+sh) / d) fits 32 bits and
+  // row_index: with 2^sh >= d, m = ceil(2^(31+sh) / d) fits 33 bits and
   // (n m) >> (31+sh) = floor(n / d) for n < 2^31
   uint32_t sh = 0;
   while ((uint64_t{1} << sh) < a.units) ++sh;
@@ -191,9 +195,10 @@ int launch_ckpt8(int kind, int dtype, Ckpt8Args a, int ranks, void* stream) {
   const uint64_t tile = kBlock * kCkptUnits, tiles = (a.rows * a.units + tile - 1) / tile;
   const uint64_t cap = 0x1000000;
   const dim3 grid((uint32_t)(tiles < cap ? tiles : cap), ranks), block(kBlock);
-#define COLL_CKPT8(K)                                                                  \
-  if (dtype == kF32) hipLaunchKernelGGL((K<kF32>), grid, block, 0, s, a);              \
-  else hipLaunchKernelGGL((K<kBF16>), grid, block, 0, s, a);                           \
+#define COLL_CKPT8(K)                                                                                \
+  if (dtype == kBF16) hipLaunchKernelGGL((K<kBF16, 8>), grid, block, 0, s, a);                       \
+  else if (elems == 4) hipLaunchKernelGGL((K<kF32, 4>), grid, block, 0, s, a);                       \
+  else hipLaunchKernelGGL((K<kF32, 8>), grid, block, 0, s, a);                                       \
   break;
   switch (kind) {
     case kCkpt8Save: COLL_CKPT8(ckpt8_save_kernel)

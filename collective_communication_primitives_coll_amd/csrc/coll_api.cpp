@@ -1465,9 +1465,9 @@ coll_status_t ckpt8_shape(size_t hidden, size_t group) {
   if (group < 16 || group > 512 || (group & (group - 1)) || hidden >= (size_t{1} << 31)) return COLL_ERR_UNSUPPORTED;
   return COLL_OK;
 }
-uint32_t group_shift(size_t group) {
+uint32_t group_log(size_t group) {
   uint32_t s = 0;
-  while ((size_t{8} << s) < group) ++s;
+  while ((size_t{1} << s) < group) ++s;
   return s;
 }
 
@@ -1488,6 +1488,29 @@ coll_status_t check_ln_shape(int p, size_t rows, size_t hidden, size_t group, bo
     st = ckpt8_shape(hidden, group);
     if (st != COLL_OK) return st;
     *ckpt_bytes = rows * fp8_row_bytes(hidden, group);
+  }
+  return COLL_OK;
+}
+
+// One of the four checkpoint kernels over all ranks; arguments as Ckpt8Args.
+coll_status_t run_ckpt8(int kind, const void* const* src, void* const* dst, void* const* again, void* const* ckpt, int p,
+                        size_t rows, size_t hidden, size_t width, size_t group, int dtype, void* stream) {
+  for (int r0 = 0; r0 < p; r0 += coll::kArgRanks) {
+    const int n = std::min(p - r0, coll::kArgRanks);
+    coll::Ckpt8Args a{};
+    for (int r = 0; r < n; ++r) {
+      if (src) a.src[r] = src[r0 + r];
+      if (dst) a.dst[r] = dst[r0 + r];
+      if (again) a.again[r] = again[r0 + r];
+      a.ckpt[r] = (uint8_t*)ckpt[r0 + r];
+    }
+    a.rows = rows;
+    a.hidden = hidden;
+    a.width = width;
+    a.row_bytes = fp8_row_bytes(hidden, group);
+    a.glog = group_log(group);
+    const int e = coll::launch_ckpt8(kind, dtype, a, n, stream);
+    if (e) return hip_fail(e);
   }
   return COLL_OK;
 }
@@ -1516,6 +1539,13 @@ coll_status_t ln_forward(const void* const* x, const void* const* gamma, const v
   if (with_ckpt) rs.add_all(ckpt, p, cbytes, true);
   st = rs.check();
   if (st != COLL_OK) return st;
+  if (with_ckpt && !coll::ln_forward_keeps(dtype, hidden, group)) {
+    // a group wider than the lanes that layer norm gives a row's unit: the
+    // checkpoint is written on its own, and first (y may be x)
+    st = run_ckpt8(coll::kCkpt8Save, x, nullptr, nullptr, ckpt, p, rows, hidden, hidden, group, dtype, stream);
+    if (st != COLL_OK) return st;
+    with_ckpt = false;
+  }
   for (int r0 = 0; r0 < p; r0 += coll::kArgRanks) {
     const int n = std::min(p - r0, coll::kArgRanks);
     coll::LnArgs a{};
@@ -1530,20 +1560,21 @@ coll_status_t ln_forward(const void* const* x, const void* const* gamma, const v
     }
     a.rows = rows;
     a.hidden = hidden;
-    a.rank0 = r0;
+    a.ranks = n;
     a.eps = eps;
     if (with_ckpt) {
       a.row_bytes = fp8_row_bytes(hidden, group);
-      a.gsh = group_shift(group);
+      a.glog = group_log(group);
     }
-    const int e = coll::launch_ln_forward(dtype, wdtype, a, n, with_ckpt, stream);
+    const int e = coll::launch_ln_forward(dtype, wdtype, a, with_ckpt, stream);
     if (e) return hip_fail(e);
   }
   return COLL_OK;
 }
 
+int ln_launches(int p) { return (p + coll::kArgRanks - 1) / coll::kArgRanks; }
 size_t ln_workspace(int p, size_t rows, size_t hidden) {
-  return (size_t)p * coll::ln_backward_groups(p, rows, hidden) * 2 * hidden * sizeof(float);
+  return (size_t)ln_launches(p) * coll::ln_backward_groups(p, rows, hidden) * 2 * hidden * sizeof(float);
 }
 
 coll_status_t ln_backward(const void* const* dy, const void* const* x, bool from_ckpt, const float* const* mean,
@@ -1597,15 +1628,15 @@ coll_status_t ln_backward(const void* const* dy, const void* const* x, bool from
       if (beta) a.beta[r] = beta[r0 + r];
       if (y) a.y[r] = y[r0 + r];
     }
-    a.ws = (float*)workspace;
+    a.ws = (float*)workspace + (size_t)(r0 / coll::kArgRanks) * groups * 2 * hidden;
     a.rows = rows;
     a.hidden = hidden;
-    a.rank0 = r0;
+    a.ranks = n;
     if (from_ckpt) {
       a.row_bytes = fp8_row_bytes(hidden, group);
-      a.gsh = group_shift(group);
+      a.glog = group_log(group);
     }
-    const int e = coll::launch_ln_backward(dtype, wdtype, a, n, groups, from_ckpt, stream);
+    const int e = coll::launch_ln_backward(dtype, wdtype, a, groups, from_ckpt, stream);
     if (e) return hip_fail(e);
   }
   if (!dgamma && !dbeta) return COLL_OK;
@@ -1616,34 +1647,10 @@ coll_status_t ln_backward(const void* const* dy, const void* const* x, bool from
   }
   j.ws = (const float*)workspace;
   j.hidden = hidden;
-  j.parts = rows ? (uint32_t)p * groups : 0;  // no rows: the sums are zero
+  j.parts = rows ? (uint32_t)ln_launches(p) * groups : 0;  // no rows: the sums are zero
   j.p = p;
   j.avg = op == COLL_AVG;
   return finish(coll::launch_ln_join(wdtype, j, stream));
-}
-
-// One of the four checkpoint kernels over all ranks.  width: elements of a
-// checkpoint row; src/dst/again as Ckpt8Args.
-coll_status_t run_ckpt8(int kind, const void* const* src, void* const* dst, void* const* again, void* const* ckpt, int p,
-                        size_t rows, size_t width, size_t units, size_t group, int dtype, void* stream) {
-  for (int r0 = 0; r0 < p; r0 += coll::kArgRanks) {
-    const int n = std::min(p - r0, coll::kArgRanks);
-    coll::Ckpt8Args a{};
-    for (int r = 0; r < n; ++r) {
-      if (src) a.src[r] = src[r0 + r];
-      if (dst) a.dst[r] = dst[r0 + r];
-      if (again) a.again[r] = again[r0 + r];
-      a.ckpt[r] = (uint8_t*)ckpt[r0 + r];
-    }
-    a.rows = rows;
-    a.hidden = width;
-    a.units = units;
-    a.row_bytes = fp8_row_bytes(width, group);
-    a.gsh = group_shift(group);
-    const int e = coll::launch_ckpt8(kind, dtype, a, n, stream);
-    if (e) return hip_fail(e);
-  }
-  return COLL_OK;
 }
 
 // Shards of a vocabulary: sizes, strides and the first index of each.
@@ -1743,7 +1750,7 @@ COLL_EXPORT coll_status_t coll_ckpt8_save(const void* const* x, void* const* ckp
   rs.add_all(ckpt, p, cbytes, true);
   st = rs.check();
   if (st != COLL_OK) return st;
-  return run_ckpt8(coll::kCkpt8Save, x, nullptr, nullptr, ckpt, p, rows, hidden, hidden / 8, group, dtype, stream);
+  return run_ckpt8(coll::kCkpt8Save, x, nullptr, nullptr, ckpt, p, rows, hidden, hidden, group, dtype, stream);
 }
 
 COLL_EXPORT coll_status_t coll_ckpt8_load(const void* const* ckpt, void* const* x, int p, size_t rows, size_t hidden,
@@ -1758,7 +1765,7 @@ COLL_EXPORT coll_status_t coll_ckpt8_load(const void* const* ckpt, void* const* 
   rs.add_all(x, p, bytes, true);
   st = rs.check();
   if (st != COLL_OK) return st;
-  return run_ckpt8(coll::kCkpt8Load, nullptr, x, nullptr, const_cast<void* const*>(ckpt), p, rows, hidden, hidden / 8,
+  return run_ckpt8(coll::kCkpt8Load, nullptr, x, nullptr, const_cast<void* const*>(ckpt), p, rows, hidden, hidden,
                    group, dtype, stream);
 }
 
@@ -1779,7 +1786,7 @@ COLL_EXPORT coll_status_t coll_swiglu_ckpt8(const void* const* gate_up, void* co
   rs.add_all(ckpt, p, cbytes, true);
   st = rs.check();
   if (st != COLL_OK) return st;
-  return run_ckpt8(coll::kSwigluForward, gate_up, out, nullptr, ckpt, p, rows, 2 * ffn, ffn / 8, group, dtype, stream);
+  return run_ckpt8(coll::kSwigluForward, gate_up, out, nullptr, ckpt, p, rows, 2 * ffn, ffn, group, dtype, stream);
 }
 
 COLL_EXPORT coll_status_t coll_swiglu_backward_ckpt8(const void* const* ckpt, const void* const* dout,
@@ -1801,7 +1808,7 @@ COLL_EXPORT coll_status_t coll_swiglu_backward_ckpt8(const void* const* ckpt, co
   rs.add_all(out, p, bytes / 2, true);
   st = rs.check();
   if (st != COLL_OK) return st;
-  return run_ckpt8(coll::kSwigluBackward, dout, dgate_up, out, const_cast<void* const*>(ckpt), p, rows, 2 * ffn, ffn / 8,
+  return run_ckpt8(coll::kSwigluBackward, dout, dgate_up, out, const_cast<void* const*>(ckpt), p, rows, 2 * ffn, ffn,
                    group, dtype, stream);
 }
 

@@ -181,12 +181,12 @@ struct LnArgs {
   void* y[kArgRanks];            // backward from a checkpoint: or null
   void* dx[kArgRanks];
   uint8_t* ckpt[kArgRanks];      // forward with a checkpoint
-  float* ws;                     // backward: partial sums [p][groups][2][hidden]
+  float* ws;                     // backward: partial sums [groups][2][hidden] of this launch
   uint64_t rows;                 // per rank
   uint64_t hidden;
   uint64_t row_bytes;            // of a checkpoint row
-  uint32_t gsh;                  // log2 of a checkpoint group's units of 8
-  int rank0;                     // the launch's first rank
+  uint32_t glog;                 // log2 of a checkpoint group's elements
+  int ranks;                     // of this launch
   float eps;
 };
 
@@ -209,15 +209,13 @@ struct Ckpt8Args {
   uint8_t* ckpt[kArgRanks];
   uint64_t rows;
   uint64_t hidden;               // elements of a checkpoint row
-  uint64_t units;                // units of 8 that a lane's walk counts per row
+  uint64_t width;                // elements that the lanes walk per row (ffn in the gated activation)
+  uint64_t units;                // units of them (set by the launcher)
   uint64_t row_bytes;
   uint64_t div_mul;              // division by units (set by the launcher)
   uint32_t div_shift;
-  uint32_t gsh;
+  uint32_t glog;                 // log2 of a group's elements
 };
-// Units of a row stay below this, so that a row's unit and a tile's offset
-// past it keep to 31 bits.
-constexpr uint64_t kCkpt8MaxUnits = uint64_t{1} << 30;
 
 // Vocabulary log probabilities over p shards.  A row's shard is cut into
 // segs[rank] pieces; all pieces of a row number at most kMaxPieces (a wave).
@@ -356,12 +354,12 @@ int launch_moe_dispatch(int elem_bytes, const MoeDirectArgs& a, int max_grid, vo
 int launch_moe_dispatch_fp8(const MoeDirectArgs& a, int max_grid, void* stream);
 int launch_moe_combine_direct(int dtype, const MoeRowArgs& a, int max_grid, void* stream);
 
-// Layer norm.  Workgroups per rank of each pass (the backward pass's also
-// fixes its workspace and so depends on the shape alone).
-uint32_t ln_forward_groups(int ranks, int tpr);
+// Layer norm.  ln_backward_groups: workgroups of each launch of the backward
+// pass (they fix its workspace, so they depend on the shape alone).
 uint32_t ln_backward_groups(int p, uint64_t rows, uint64_t hidden);
-int launch_ln_forward(int dtype, int wdtype, const LnArgs& a, int ranks, bool ckpt, void* stream);
-int launch_ln_backward(int dtype, int wdtype, const LnArgs& a, int ranks, uint32_t groups, bool ckpt, void* stream);
+bool ln_forward_keeps(int dtype, uint64_t hidden, uint64_t group);
+int launch_ln_forward(int dtype, int wdtype, const LnArgs& a, bool ckpt, void* stream);
+int launch_ln_backward(int dtype, int wdtype, const LnArgs& a, uint32_t groups, bool ckpt, void* stream);
 int launch_ln_join(int wdtype, const LnJoinArgs& a, void* stream);
 
 // 8-bit checkpoints and the gated activation (kind: Ckpt8Kind).

@@ -10,7 +10,7 @@
 // Bound by HBM: 4 bytes an element forward and 6 backward in bf16, against
 // some 10 fp32 operations.  So every row is read once: it stays in
 // registers between its statistics and its result, TPR lanes to a row, each
-// with one or two units of 8 elements.
+// with 8 or 16 elements of it.
 //
 // The backward pass keeps a lane on the same columns for all rows of its
 // workgroup, so that the weights' gradients build up in its registers.  At
@@ -22,6 +22,7 @@
 //
 // All sums are fp32 (a lane's partial sums run over at most a few hundred
 // rows before the join); bf16 results are narrowed once.
+#include <algorithm>
 #include <type_traits>
 
 #include "token_unit.h"
@@ -31,147 +32,250 @@ namespace coll {
 namespace {
 
 constexpr int block_of(int tpr) { return tpr < kBlock ? kBlock : tpr; }
+constexpr int waves_of(int tpr) { return tpr < kWave ? 1 : tpr / kWave; }
 
-// Sum over the TPR lanes of a row.  red: TPR / 64 floats of LDS.  One
-// barrier: a caller alternates between two arrays, so that a wave that
-// writes an array again has passed a barrier that every wave reached after
-// reading it.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-  v = wave_sum(v);
-  if constexpr (TPR > kWave) {
-    constexpr int NW = TPR / kWave;
-    if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
-    __syncthreads();
-    v = 0.0f;
+// Sums over the TPR lanes of a row, R at once.  red: LDS.  One barrier: a
+// caller alternates between two arrays, so that a wave that writes an array
+// again has passed a barrier that every wave reached after reading it.
+template <int TPR, int R>
+__device__ __forceinline__ void row_sums(float (&v)[R], float (&red)[R][waves_of(TPR)]) {
 #pragma unroll
-    for (int w = 0; w < NW; ++w) v += red[w];
+  for (int k = 0; k < R; ++k) v[k] = wave_sum<std::min(TPR, kWave)>(v[k]);
+  if constexpr (TPR > kWave) {
+    if (threadIdx.x % kWave == 0) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) red[k][threadIdx.x / kWave] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      v[k] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < TPR / kWave; ++w) v[k] += red[k][w];
+    }
   }
-  return v;
 }
 
-// Unit u of a row, zeros past its end.  full: whole units of the row.
-template <int SRC, bool TAIL, bool NT>
-__device__ __forceinline__ RawUnit<SRC> row_unit(const void* row, uint64_t u, uint64_t full, uint32_t part, uint64_t hidden,
-                                                 uint32_t gsh) {
-  if (u < full) {
-    if constexpr (SRC == kE4M3) return load_codes<NT>(static_cast<const uint8_t*>(row), hidden, u, gsh);
-    else return load_unit<SRC, NT>(row, u);
+// A row of the register-resident kernels, E elements to a unit.  Without a
+// tail (hidden a multiple of E) it is a bounded buffer.  With one, or where
+// a wave holds several rows and no one buffer, a lane
+// whose unit reaches past the end takes the row's last E elements instead:
+// every lane then loads and stores whole units (the elements it shares with
+// a neighbour get the same values from both), and only the sums leave out
+// the first skip_of() elements, which are not its own.
+template <int SRC, int E, bool TAIL>
+struct Row;
+template <int DT, int E>
+struct Row<DT, E, false> {
+  RowBuffer b;
+  __device__ __forceinline__ Row(const void* base, uint32_t hidden, uint32_t = 0) : b(base, hidden * Traits<DT>::B) {}
+  template <bool NT>
+  __device__ __forceinline__ RawUnit<DT, E> get(uint32_t u) const { return load_unit<DT, E, NT>(b, u * E); }
+  template <bool NT>
+  __device__ __forceinline__ void put(uint32_t u, const RawUnit<DT, E>& r) const { store_unit<DT, E, NT>(b, u * E, r); }
+};
+template <int DT, int E>
+struct Row<DT, E, true> {
+  uint8_t* base;
+  uint32_t last;  // first element of the row's last E
+  __device__ __forceinline__ Row(const void* p, uint32_t hidden, uint32_t = 0) : base((uint8_t*)p), last(hidden - E) {}
+  template <bool NT>
+  __device__ __forceinline__ RawUnit<DT, E> get(uint32_t u) const {
+    return load_unit<DT, E, NT>((const void*)base, min(E * u, last));
   }
-  if constexpr (TAIL && SRC != kE4M3)
-    if (u == full) return load_part<SRC>(row, u, part);
-  return zero_unit<SRC>();
+  template <bool NT>
+  __device__ __forceinline__ void put(uint32_t u, const RawUnit<DT, E>& r) const {
+    store_unit<DT, E, NT>((void*)base, min(E * u, last), r);
+  }
+};
+template <int E>
+struct Row<kE4M3, E, false> {
+  RowBuffer codes, scales;
+  uint32_t glog;
+  __device__ __forceinline__ Row(const void* base, uint32_t hidden, uint32_t g)
+      : codes(base, hidden), scales((const uint8_t*)base + hidden, (hidden >> g) * 4), glog(g) {}
+  template <bool NT>
+  __device__ __forceinline__ RawUnit<kE4M3, E> get(uint32_t u) const { return load_codes<E, NT>(codes, scales, u * E, glog); }
+};
+
+template <int E>
+struct Row<kE4M3, E, true> {
+  const uint8_t* base;
+  uint32_t hidden, glog;
+  __device__ __forceinline__ Row(const void* p, uint32_t h, uint32_t g) : base((const uint8_t*)p), hidden(h), glog(g) {}
+  template <bool NT>
+  __device__ __forceinline__ RawUnit<kE4M3, E> get(uint32_t u) const {
+    return load_codes<E, NT>(base, hidden, min(E * u, hidden - E), glog);
+  }
+};
+
+// Elements of unit u that a row with a tail leaves out of its sums (E: all).
+template <int E>
+__device__ __forceinline__ uint32_t skip_of(uint32_t u, uint32_t hidden) {
+  return E * u > hidden - E ? min(E * u - (hidden - E), (uint32_t)E) : 0;
 }
-template <int DT, bool TAIL, bool NT>
-__device__ __forceinline__ void put_unit(void* row, uint64_t u, uint64_t full, uint32_t part, const float (&f)[8]) {
-  if (u < full) store_unit<DT, NT>(row, u, narrow_unit<DT>(f));
-  else if constexpr (TAIL)
-    if (u == full) store_part<DT>(row, u, part, f);
-}
+// Whether the i-th of a lane's NU units can reach past the end: row_shape
+// fills at least half of the lanes' units, except in its narrow classes.
+template <int TPR, int NU>
+constexpr bool may_end(int i) { return TPR <= kWave || NU == 1 || 2 * i >= NU; }
 
 // A weight vector's units of this lane (ones or zeros where it is absent).
-template <int WT, bool TAIL, int NU, int TPR>
-__device__ __forceinline__ void load_weights(const void* w, float absent, uint32_t lane, uint32_t full, uint32_t part,
-                                             RawUnit<WT> (&out)[NU]) {
-  float f[8];
+template <int WT, int E, bool TAIL, int NU, int TPR>
+__device__ __forceinline__ void load_weights(const void* w, float absent, uint32_t lane, uint32_t hidden,
+                                             RawUnit<WT, E> (&out)[NU]) {
+  if (w) {
+    const Row<WT, E, TAIL> row(w, hidden);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = absent;
+    for (int i = 0; i < NU; ++i) out[i] = row.template get<false>(i * TPR + lane);
+  } else {
+    float f[E];
 #pragma unroll
-  for (int i = 0; i < NU; ++i)
-    out[i] = w ? row_unit<WT, TAIL, false>(w, i * TPR + lane, full, part, 0, 0) : narrow_unit<WT>(f);
+    for (int e = 0; e < E; ++e) f[e] = absent;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) out[i] = narrow_unit<WT, E>(f);
+  }
 }
 
-// Whether a row's loads are issued before the sums of the row before it: a
-// workgroup of 1024 lanes has no registers left for them.
+// The row of this lane's group: workgroups take block_of(TPR) / TPR rows at
+// a time.
 template <int TPR>
-constexpr bool kAhead = TPR < 1024;
+__device__ __forceinline__ uint64_t own_row(uint64_t block) {
+  if constexpr (TPR >= kBlock) return block;
+  if constexpr (TPR < kWave) return block * (kBlock / TPR) + threadIdx.x / TPR;
+  return block * (kBlock / TPR) + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+}
 
 // ---------------------------------------------------------------------------
-// Forward.  Grid (workgroups, ranks); a workgroup takes every gridDim.x-th
-// run of its rows, the next row's loads issued before this row's sums.
+// Forward.  Grid (runs of rows, ranks), and no walk: the workgroups that
+// share a CU hide each other's waits, and a workgroup that ends waits for no
+// store.  A lane holds the same columns of kRows rows, so that the weights
+// are loaded once for them, and it asks for the weights only after the first
+// sums: loads return in order, and the weights, though they come from L2,
+// queue behind other waves' rows.
+// 8 x 4096 x 7168 bf16: 152 us (6.2 TB/s; the card's 1:1 streams reach 6.3).
+// One row at a time 158 us, and 173 us with the weights asked for first;
+// three rows 155, four 159.  Persistent workgroups, with the weights in
+// registers and the next row's loads ahead, 166-175 us; rows claimed from
+// counters 158-164 us.
+// With the checkpoint, 8 x 2048 x 7168 bf16 and fp32 weights: 113 us
+// (5.3 TB/s), bound by how many rows the registers hold.
 // ---------------------------------------------------------------------------
+constexpr int kRows = 2;
+
 template <int DT, int WT, int TPR, int NU, bool TAIL, bool CKPT>
 __global__ __launch_bounds__(block_of(TPR)) void ln_forward_kernel(LnArgs a) {
-  constexpr int RPB = block_of(TPR) / TPR;
-  __shared__ float red[2][TPR / kWave];
+  constexpr int E = kElems<DT>;
+  __shared__ float red[2][kRows][waves_of(TPR)];
   const int rank = blockIdx.y;
-  const uint32_t lane = threadIdx.x % TPR;
-  const uint32_t H = (uint32_t)a.hidden, full = H / 8, part = H % 8;
-  const uint64_t stride = (uint64_t)gridDim.x * RPB, row_bytes = (uint64_t)H * Traits<DT>::B;
-  const uint8_t* x = static_cast<const uint8_t*>(a.x[rank]);
-  uint64_t row = (uint64_t)blockIdx.x * RPB + (RPB > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0);
-  if (row >= a.rows) return;
-  RawUnit<DT> cur[NU], nxt[NU];
+  const uint32_t lane = threadIdx.x % TPR, H = (uint32_t)a.hidden;
+  const uint64_t row_bytes = (uint64_t)H * Traits<DT>::B;
+  const uint64_t row0 = own_row<TPR>(blockIdx.x) * kRows;
+  if (row0 >= a.rows) return;
+  const uint8_t* x0 = static_cast<const uint8_t*>(a.x[rank]) + row0 * row_bytes;
+  RawUnit<DT, E> raw[kRows][NU];
 #pragma unroll
-  for (int i = 0; i < NU; ++i) cur[i] = row_unit<DT, TAIL, true>(x + row * row_bytes, i * TPR + lane, full, part, 0, 0);
-  RawUnit<WT> gamma[NU], beta[NU];
-  load_weights<WT, TAIL, NU, TPR>(a.gamma[rank], 1.0f, lane, full, part, gamma);
-  load_weights<WT, TAIL, NU, TPR>(a.beta[rank], 0.0f, lane, full, part, beta);
-  while (true) {
-    const uint64_t next = row + stride;
-    const bool more = next < a.rows;
-    auto fetch = [&] {
+  for (int k = 0; k < kRows; ++k) {
+    // past the last row: row0 again (its results are not stored)
+    const Row<DT, E, TAIL> x(x0 + (row0 + k < a.rows ? k : 0) * row_bytes, H);
 #pragma unroll
-      for (int i = 0; i < NU; ++i)
-        nxt[i] = row_unit<DT, TAIL, true>(x + next * row_bytes, i * TPR + lane, full, part, 0, 0);
-    };
-    if (kAhead<TPR> && more) fetch();
-    float f[NU][8], s = 0.0f;
+    for (int i = 0; i < NU; ++i) raw[k][i] = x.template get<true>(i * TPR + lane);
+  }
+  float f[kRows][NU][E], s[kRows], q[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    s[k] = 0.0f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      widen_unit(cur[i], f[i]);
+      const uint32_t u = i * TPR + lane, skip = TAIL && may_end<TPR, NU>(i) ? skip_of<E>(u, H) : 0;
+      widen_unit(raw[k][i], f[k][i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += f[i][e];
+      for (uint32_t e = 0; e < E; ++e) s[k] += TAIL && may_end<TPR, NU>(i) && e < skip ? 0.0f : f[k][i][e];
+      if constexpr (CKPT) {
+        const RawUnit<kE4M3, E> code = encode_unit<DT, E>(raw[k][i], f[k][i], a.glog);
+        if (E * u < H && row0 + k < a.rows)
+          store_codes<E, true>(a.ckpt[rank] + (row0 + k) * a.row_bytes, H, a.row_bytes, E * u, a.glog, code);
+      }
     }
-    const float mean = row_sum<TPR>(s, red[0]) / (float)H;
+  }
+  row_sums<TPR, kRows>(s, red[0]);
+  RawUnit<WT, E> gamma[NU], beta[NU];
+  load_weights<WT, E, TAIL, NU, TPR>(a.gamma[rank], 1.0f, lane, H, gamma);
+  load_weights<WT, E, TAIL, NU, TPR>(a.beta[rank], 0.0f, lane, H, beta);
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    s[k] /= (float)H;
     // the deviations' squares, not the squares' mean less the mean's
     // square, which cancels where the mean is large
-    float q = 0.0f;
+    q[k] = 0.0f;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t u = i * TPR + lane;
-      const uint32_t cnt = u < full ? 8u : (TAIL && u == full) ? part : 0u;
+      const uint32_t u = i * TPR + lane, skip = TAIL && may_end<TPR, NU>(i) ? skip_of<E>(u, H) : 0;
+      float sq = 0.0f;
 #pragma unroll
-      for (uint32_t e = 0; e < 8; ++e) {
-        const float d = f[i][e] - mean;
-        if (TAIL ? e < cnt : cnt != 0) q += d * d;
+      for (uint32_t e = 0; e < E; ++e) {
+        const float d = f[k][i][e] - s[k];
+        sq = TAIL && may_end<TPR, NU>(i) && e < skip ? sq : __builtin_fmaf(d, d, sq);
       }
+      q[k] += !TAIL && E * u >= H ? 0.0f : sq;
     }
-    const float rstd = rsqrtf(row_sum<TPR>(q, red[1]) / (float)H + a.eps);
-    uint8_t* y = static_cast<uint8_t*>(a.y[rank]) + row * row_bytes;
+  }
+  row_sums<TPR, kRows>(q, red[1]);
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if (row0 + k >= a.rows) break;
+    const float rstd = rsqrtf(q[k] / (float)H + a.eps);
+    const Row<DT, E, TAIL> y(static_cast<uint8_t*>(a.y[rank]) + (row0 + k) * row_bytes, H);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const uint32_t u = i * TPR + lane;
-      if constexpr (CKPT) {
-        const RawUnit<kE4M3> code = encode_unit<DT>(cur[i], f[i], a.gsh);
-        if (u < full) store_codes<true>(a.ckpt[rank] + row * a.row_bytes, H, a.row_bytes, u, a.gsh, code);
-      }
-      float g[8], b[8];
+      float g[E], b[E];
       widen_unit(gamma[i], g);
       widen_unit(beta[i], b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = (f[i][e] - mean) * rstd * g[e] + b[e];
-      put_unit<DT, TAIL, true>(y, u, full, part, f[i]);
+      for (int e = 0; e < E; ++e) f[k][i][e] = (f[k][i][e] - s[k]) * rstd * g[e] + b[e];
+      y.template put<true>(i * TPR + lane, narrow_unit<DT, E>(f[k][i]));
     }
     if (lane == 0) {
-      if (a.mean[rank]) as_global(a.mean[rank])[row] = mean;
-      if (a.rstd[rank]) as_global(a.rstd[rank])[row] = rstd;
+      if (a.mean[rank]) as_global(a.mean[rank])[row0 + k] = s[k];
+      if (a.rstd[rank]) as_global(a.rstd[rank])[row0 + k] = rstd;
     }
-    if (!more) break;
-    if (!kAhead<TPR>) fetch();
-    row = next;
-#pragma unroll
-    for (int i = 0; i < NU; ++i) cur[i] = nxt[i];
   }
 }
 
-// Rows too wide for the registers: a workgroup of 1024 goes over the row
-// three times (sum, deviations, result); the later two find it in the
-// caches.
+// ---------------------------------------------------------------------------
+// Rows too wide for the registers (or narrower than one unit): units of 8
+// elements in every type, each row gone over several times; all passes but
+// the first find it in the caches.
+// ---------------------------------------------------------------------------
+
+// Unit u of a row in memory, zeros past its end.  full: whole units of the
+// row; part: elements of its last, partial unit.
+template <int SRC>
+__device__ __forceinline__ RawUnit<SRC, 8> row_unit(const void* row, uint64_t u, uint64_t full, uint32_t part, uint64_t hidden = 0,
+                                                    uint32_t glog = 0) {
+  if constexpr (SRC == kE4M3) {
+    if (u < full) return load_codes<8, false>(static_cast<const uint8_t*>(row), hidden, u * 8, glog);
+  } else {
+    if (u < full) return load_unit<SRC, 8, false>(row, u * 8);
+    if (u == full) return load_part<SRC, 8>(row, u * 8, part);
+  }
+  return zero_unit<SRC, 8>();
+}
+template <int DT>
+__device__ __forceinline__ void put_unit(void* row, uint64_t u, uint64_t full, uint32_t part, const float (&f)[8]) {
+  if (u < full) store_unit<DT, 8, false>(row, u * 8, narrow_unit<DT, 8>(f));
+  else if (u == full) store_part<DT, 8>(row, u * 8, part, f);
+}
+template <int WT>
+__device__ __forceinline__ void weight_unit(const void* w, float absent, uint64_t u, uint64_t full, uint32_t part, float (&f)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = absent;
+  if (w) widen_unit(row_unit<WT>(w, u, full, part), f);
+}
+
 template <int DT, int WT, bool CKPT>
 __global__ __launch_bounds__(1024) void ln_forward_wide_kernel(LnArgs a) {
   constexpr int TPR = 1024;
-  __shared__ float red[2][TPR / kWave];
+  __shared__ float red[2][1][TPR / kWave];
   const int rank = blockIdx.y;
   const uint64_t H = a.hidden, full = H / 8, units = (H + 7) / 8;
   const uint32_t part = (uint32_t)(H % 8);
@@ -180,42 +284,38 @@ __global__ __launch_bounds__(1024) void ln_forward_wide_kernel(LnArgs a) {
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const uint8_t* x = static_cast<const uint8_t*>(a.x[rank]) + row * H * Traits<DT>::B;
     uint8_t* y = static_cast<uint8_t*>(a.y[rank]) + row * H * Traits<DT>::B;
-    float f[8], s = 0.0f;
+    float f[8], s[1] = {0.0f}, q[1] = {0.0f};
     for (uint64_t k = 0; k < steps; ++k) {
-      widen_unit(row_unit<DT, true, false>(x, k * TPR + threadIdx.x, full, part, 0, 0), f);
+      widen_unit(row_unit<DT>(x, k * TPR + threadIdx.x, full, part), f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += f[e];
+      for (int e = 0; e < 8; ++e) s[0] += f[e];
     }
-    const float mean = row_sum<TPR>(s, red[0]) / (float)H;
-    float q = 0.0f;
+    row_sums<TPR, 1>(s, red[0]);
+    const float mean = s[0] / (float)H;
     for (uint64_t k = 0; k < steps; ++k) {
       const uint64_t u = k * TPR + threadIdx.x;
       const uint32_t cnt = u < full ? 8u : u == full ? part : 0u;
-      widen_unit(row_unit<DT, true, false>(x, u, full, part, 0, 0), f);
+      widen_unit(row_unit<DT>(x, u, full, part), f);
 #pragma unroll
       for (uint32_t e = 0; e < 8; ++e)
-        if (e < cnt) q += (f[e] - mean) * (f[e] - mean);
+        if (e < cnt) q[0] += (f[e] - mean) * (f[e] - mean);
     }
-    const float rstd = rsqrtf(row_sum<TPR>(q, red[1]) / (float)H + a.eps);
+    row_sums<TPR, 1>(q, red[1]);
+    const float rstd = rsqrtf(q[0] / (float)H + a.eps);
     for (uint64_t k = 0; k < steps; ++k) {
       const uint64_t u = k * TPR + threadIdx.x;
-      const RawUnit<DT> raw = row_unit<DT, true, false>(x, u, full, part, 0, 0);
+      const RawUnit<DT, 8> raw = row_unit<DT>(x, u, full, part);
       widen_unit(raw, f);
       if constexpr (CKPT) {
-        const RawUnit<kE4M3> code = encode_unit<DT>(raw, f, a.gsh);
-        if (u < full) store_codes<true>(a.ckpt[rank] + row * a.row_bytes, H, a.row_bytes, u, a.gsh, code);
+        const RawUnit<kE4M3, 8> code = encode_unit<DT, 8>(raw, f, a.glog);
+        if (u < full) store_codes<8, true>(a.ckpt[rank] + row * a.row_bytes, H, a.row_bytes, u * 8, a.glog, code);
       }
       float g[8], b[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        g[e] = 1.0f;
-        b[e] = 0.0f;
-      }
-      if (a.gamma[rank]) widen_unit(row_unit<WT, true, false>(a.gamma[rank], u, full, part, 0, 0), g);
-      if (a.beta[rank]) widen_unit(row_unit<WT, true, false>(a.beta[rank], u, full, part, 0, 0), b);
+      weight_unit<WT>(a.gamma[rank], 1.0f, u, full, part, g);
+      weight_unit<WT>(a.beta[rank], 0.0f, u, full, part, b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = (f[e] - mean) * rstd * g[e] + b[e];
-      put_unit<DT, true, false>(y, u, full, part, f);
+      put_unit<DT>(y, u, full, part, f);
     }
     if (threadIdx.x == 0) {
       if (a.mean[rank]) as_global(a.mean[rank])[row] = mean;
@@ -225,149 +325,152 @@ __global__ __launch_bounds__(1024) void ln_forward_wide_kernel(LnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Backward.  Partial sums of workgroup (b, rank) go to
-// ws[rank0 + rank][b][0: dgamma, 1: dbeta][hidden].
+// Backward.  A workgroup takes every gridDim.x-th run of rows, through all
+// ranks of the launch: the rows in work at any time lie close together.
+// Partial sums of workgroup b go to ws[b][0: dgamma, 1: dbeta][hidden].
 // ---------------------------------------------------------------------------
-template <int TAILS>
-__device__ __forceinline__ void put_partial(float* ws, uint64_t u, uint64_t full, uint32_t part, const float (&f)[8]) {
-  put_unit<kF32, TAILS != 0, false>(ws, u, full, part, f);
-}
+
+// Rows whose loads are issued ahead of the row in work: a workgroup of 1024
+// lanes has no registers left for one.  Two ahead, with as many registers
+// more, were not faster.
+template <int TPR>
+constexpr int kAhead = TPR < 1024 ? 1 : 0;
 
 template <int SRC, int DT, int WT, int TPR, int NU, bool TAIL>
 __global__ __launch_bounds__(block_of(TPR)) void ln_backward_kernel(LnArgs a) {
-  constexpr bool AHEAD = kAhead<TPR>;
-  constexpr int RPB = block_of(TPR) / TPR;
-  __shared__ float red[2][2][TPR / kWave];
-  __shared__ float fold[RPB > 1 ? 2 * NU * TPR * 8 : 1];
-  const int rank = blockIdx.y;
-  const uint32_t lane = threadIdx.x % TPR;
-  const uint32_t H = (uint32_t)a.hidden, full = H / 8, part = H % 8;
-  const uint64_t stride = (uint64_t)gridDim.x * RPB, row_bytes = (uint64_t)H * Traits<DT>::B;
-  const uint64_t src_bytes = SRC == kE4M3 ? a.row_bytes : row_bytes;
-  const uint8_t* x = static_cast<const uint8_t*>(a.x[rank]);
-  const uint8_t* dy = static_cast<const uint8_t*>(a.dy[rank]);
-  const int mine = RPB > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
-  uint64_t row = (uint64_t)blockIdx.x * RPB + mine;
-  float dg[NU][8] = {}, db[NU][8] = {};
-  if (row < a.rows) {
-    RawUnit<SRC> cx[NU], nx[NU];
-    RawUnit<DT> cd[NU], nd[NU];
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      cx[i] = row_unit<SRC, TAIL, true>(x + row * src_bytes, i * TPR + lane, full, part, H, a.gsh);
-      cd[i] = row_unit<DT, TAIL, true>(dy + row * row_bytes, i * TPR + lane, full, part, 0, 0);
-    }
-    float mean = as_global(a.mean[rank])[row], rstd = as_global(a.rstd[rank])[row];
-    RawUnit<WT> gamma[NU];
-    load_weights<WT, TAIL, NU, TPR>(a.gamma[rank], 1.0f, lane, full, part, gamma);
-    int turn = 0;
-    while (true) {
-      const uint64_t next = row + stride;
-      const bool more = next < a.rows;
-      float nmean = 0.0f, nrstd = 0.0f;
-      auto fetch = [&] {
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-          nx[i] = row_unit<SRC, TAIL, true>(x + next * src_bytes, i * TPR + lane, full, part, H, a.gsh);
-          nd[i] = row_unit<DT, TAIL, true>(dy + next * row_bytes, i * TPR + lane, full, part, 0, 0);
-        }
-        nmean = as_global(a.mean[rank])[next];
-        nrstd = as_global(a.rstd[rank])[next];
-      };
-      if (AHEAD && more) fetch();
-      float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        float fx[8], fd[8], g[8];
-        widen_unit(cx[i], fx);
-        widen_unit(cd[i], fd);
-        widen_unit(gamma[i], g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          // past the row's end dy is zero, and so is all that it enters
-          const float n = (fx[e] - mean) * rstd, w = fd[e] * g[e];
-          dg[i][e] += fd[e] * n;
-          db[i][e] += fd[e];
-          s1 += w;
-          s2 += w * n;
-        }
-      }
-      s1 = wave_sum(s1);
-      s2 = wave_sum(s2);
-      if constexpr (TPR > kWave) {
-        constexpr int NW = TPR / kWave;
-        if (threadIdx.x % kWave == 0) {
-          red[turn][0][threadIdx.x / kWave] = s1;
-          red[turn][1][threadIdx.x / kWave] = s2;
-        }
-        __syncthreads();
-        s1 = s2 = 0.0f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          s1 += red[turn][0][w];
-          s2 += red[turn][1][w];
-        }
-        turn ^= 1;
-      }
-      const float c1 = s1 / (float)H, c2 = s2 / (float)H;
-      uint8_t* dx = static_cast<uint8_t*>(a.dx[rank]) + row * row_bytes;
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        const uint32_t u = i * TPR + lane;
-        float fx[8], fd[8], g[8];
-        widen_unit(cx[i], fx);
-        widen_unit(cd[i], fd);
-        widen_unit(gamma[i], g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float n = (fx[e] - mean) * rstd;
-          fd[e] = rstd * (fd[e] * g[e] - c1 - n * c2);
-          fx[e] = n;
-        }
-        put_unit<DT, TAIL, true>(dx, u, full, part, fd);
-        if constexpr (SRC == kE4M3) {
-          // the output again, for the weight gradient of the product it fed
-          if (a.y[rank]) {
-            RawUnit<WT> bu[1];
-            float b[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[e] = 0.0f;
-            if (a.beta[rank]) {
-              bu[0] = row_unit<WT, TAIL, false>(a.beta[rank], u, full, part, 0, 0);
-              widen_unit(bu[0], b);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) fx[e] = fx[e] * g[e] + b[e];
-            put_unit<DT, TAIL, true>(static_cast<uint8_t*>(a.y[rank]) + row * row_bytes, u, full, part, fx);
-          }
-        }
-      }
-      if (!more) break;
-      if (!AHEAD) fetch();
-      row = next;
-      mean = nmean;
-      rstd = nrstd;
-#pragma unroll
-      for (int i = 0; i < NU; ++i) {
-        cx[i] = nx[i];
-        cd[i] = nd[i];
+  constexpr int E = kElems<DT>, RPB = block_of(TPR) / TPR, AHEAD = kAhead<TPR>;
+  __shared__ float red[2][2][waves_of(TPR)];
+  __shared__ float fold[RPB > 1 ? 2 * NU * E * TPR : 1];
+  const uint32_t lane = threadIdx.x % TPR, H = (uint32_t)a.hidden;
+  const uint64_t row_bytes = (uint64_t)H * Traits<DT>::B, src_bytes = SRC == kE4M3 ? a.row_bytes : row_bytes;
+  const uint64_t stride = (uint64_t)gridDim.x * RPB;
+  // a place in the ranks' rows, one rank after the other
+  struct Place {
+    uint64_t row;
+    int rank;
+    __device__ __forceinline__ void settle(const LnArgs& a) {
+      while (row >= a.rows && rank < a.ranks) {
+        row -= a.rows;
+        ++rank;
       }
     }
-  }
-  float* ws = a.ws + ((uint64_t)(a.rank0 + rank) * gridDim.x + blockIdx.x) * 2 * H;
-  if constexpr (RPB > 1) {
-    // the workgroup's waves add their sums in turn
-    for (int w = 0; w < RPB; ++w) {
-      if (mine == w) {
+  };
+  Place at{own_row<TPR>(blockIdx.x), 0};
+  at.settle(a);
+  float dg[NU][E] = {}, db[NU][E] = {};
+  if (at.rank < a.ranks) {
+    // AHEAD + 1 buffers; the loop is unrolled over them, since moving a
+    // loaded register to another waits for its load
+    RawUnit<SRC, E> bx[AHEAD + 1][NU];
+    RawUnit<DT, E> bd[AHEAD + 1][NU];
+    float bm[AHEAD + 1], bs[AHEAD + 1];
+    auto fetch = [&](const Place& r, auto K) {
+      constexpr int k = decltype(K)::value;
+      const Row<SRC, E, TAIL> rx(static_cast<const uint8_t*>(a.x[r.rank]) + r.row * src_bytes, H, a.glog);
+      const Row<DT, E, TAIL> rd(static_cast<const uint8_t*>(a.dy[r.rank]) + r.row * row_bytes, H);
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        bx[k][i] = rx.template get<true>(i * TPR + lane);
+        bd[k][i] = rd.template get<true>(i * TPR + lane);
+      }
+      bm[k] = ld_const(a.mean[r.rank] + r.row);
+      bs[k] = ld_const(a.rstd[r.rank] + r.row);
+    };
+    fetch(at, std::integral_constant<int, 0>());
+    RawUnit<WT, E> gamma[NU];
+    int held = -1, turn = 0;
+    // one row from buffer K; whether there is another
+    auto step = [&](auto K) {
+      constexpr int k = decltype(K)::value;
+      if (at.rank != held) {
+        held = at.rank;
+        load_weights<WT, E, TAIL, NU, TPR>(a.gamma[held], 1.0f, lane, H, gamma);
 #pragma unroll
         for (int i = 0; i < NU; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float* at = fold + (i * 8 + e) * TPR + lane;
-            dg[i][e] += w ? at[0] : 0.0f;
-            db[i][e] += w ? at[NU * 8 * TPR] : 0.0f;
-            at[0] = dg[i][e];
-            at[NU * 8 * TPR] = db[i][e];
+          for (auto& v : gamma[i].v) asm volatile("" : "+v"(v));  // waited for here, not in every step
+      }
+      // after the last row: that row again, so that every step issues the
+      // same and the compiler can count what it waits for
+      Place next{at.row + stride, at.rank};
+      next.settle(a);
+      const bool more = next.rank < a.ranks;
+      if (!more) next = at;
+      if constexpr (AHEAD > 0) fetch(next, std::integral_constant<int, (k + 1) % (AHEAD + 1)>());
+      const float mean = bm[k], rstd = bs[k];
+      float n[NU][E], w[NU][E], s[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        const uint32_t skip = TAIL && may_end<TPR, NU>(i) ? skip_of<E>(i * TPR + lane, H) : 0;
+        float d[E], g[E];
+        widen_unit(bx[k][i], n[i]);
+        widen_unit(bd[k][i], d);
+        widen_unit(gamma[i], g);
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e) {
+          n[i][e] = (n[i][e] - mean) * rstd;
+          w[i][e] = d[e] * g[e];
+          // past the row's end dy is zero, and so is all that it enters
+          const bool own = !(TAIL && may_end<TPR, NU>(i) && e < skip);
+          const float de = own ? d[e] : 0.0f, we = own ? w[i][e] : 0.0f;
+          dg[i][e] += own ? de * n[i][e] : 0.0f;
+          db[i][e] += de;
+          s[0] += we;
+          s[1] += own ? we * n[i][e] : 0.0f;
+        }
+      }
+      row_sums<TPR, 2>(s, red[turn]);
+      turn ^= 1;
+      const float c1 = s[0] / (float)H, c2 = s[1] / (float)H;
+      const Row<DT, E, TAIL> dx(static_cast<uint8_t*>(a.dx[at.rank]) + at.row * row_bytes, H);
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[i][e] = rstd * (w[i][e] - c1 - n[i][e] * c2);
+        dx.template put<true>(i * TPR + lane, narrow_unit<DT, E>(w[i]));
+      }
+      if constexpr (SRC == kE4M3) {
+        // the output again, for the weight gradient of the product it fed
+        if (a.y[at.rank]) {
+          const Row<DT, E, TAIL> y(static_cast<uint8_t*>(a.y[at.rank]) + at.row * row_bytes, H);
+          RawUnit<WT, E> beta[NU];
+          load_weights<WT, E, TAIL, NU, TPR>(a.beta[at.rank], 0.0f, lane, H, beta);
+#pragma unroll
+          for (int i = 0; i < NU; ++i) {
+            float g[E], b[E];
+            widen_unit(gamma[i], g);
+            widen_unit(beta[i], b);
+#pragma unroll
+            for (int e = 0; e < E; ++e) n[i][e] = n[i][e] * g[e] + b[e];
+            y.template put<true>(i * TPR + lane, narrow_unit<DT, E>(n[i]));
+          }
+        }
+      }
+      if constexpr (AHEAD == 0) fetch(next, K);
+      at = next;
+      return more;
+    };
+    while (true) {
+      if (!step(std::integral_constant<int, 0>())) break;
+      if constexpr (AHEAD > 0)
+        if (!step(std::integral_constant<int, 1>())) break;
+    }
+  }
+  float* ws = a.ws + (uint64_t)blockIdx.x * 2 * H;
+  if constexpr (RPB > 1) {
+    // the workgroup's groups of lanes add their sums in turn
+    const int mine = (int)own_row<TPR>(0);
+    for (int k = 0; k < RPB; ++k) {
+      if (mine == k) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            float* to = fold + (i * E + e) * TPR + lane;
+            dg[i][e] += k ? to[0] : 0.0f;
+            db[i][e] += k ? to[NU * E * TPR] : 0.0f;
+            to[0] = dg[i][e];
+            to[NU * E * TPR] = db[i][e];
           }
       }
       __syncthreads();
@@ -376,8 +479,20 @@ __global__ __launch_bounds__(block_of(TPR)) void ln_backward_kernel(LnArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    put_partial<TAIL>(ws, i * TPR + lane, full, part, dg[i]);
-    put_partial<TAIL>(ws + H, i * TPR + lane, full, part, db[i]);
+    const uint32_t u = i * TPR + lane;
+    if (E * u + E <= H) {
+      store_unit<kF32, E, false>((void*)ws, E * u, narrow_unit<kF32, E>(dg[i]));
+      store_unit<kF32, E, false>((void*)(ws + H), E * u, narrow_unit<kF32, E>(db[i]));
+    } else if (TAIL && E * u < H) {
+      // the row's last E elements, of which the last H % E are this unit's
+      const uint32_t skip = skip_of<E>(u, H);
+#pragma unroll
+      for (uint32_t e = 0; e < E; ++e)
+        if (e >= skip) {
+          as_global(ws)[H - E + e] = dg[i][e];
+          as_global(ws)[2 * (uint64_t)H - E + e] = db[i][e];
+        }
+    }
   }
 }
 
@@ -387,47 +502,46 @@ __global__ __launch_bounds__(block_of(TPR)) void ln_backward_kernel(LnArgs a) {
 // dy's own buffer.
 template <int SRC, int DT>
 __global__ __launch_bounds__(kBlock) void ln_backward_wide_columns_kernel(LnArgs a, uint32_t splits) {
-  const int rank = blockIdx.y;
   const uint64_t H = a.hidden, full = H / 8, row_bytes = H * Traits<DT>::B;
   const uint64_t src_bytes = SRC == kE4M3 ? a.row_bytes : row_bytes;
   const uint32_t part = (uint32_t)(H % 8), split = blockIdx.x % splits;
   const uint64_t u = (uint64_t)(blockIdx.x / splits) * kBlock + threadIdx.x;
   float dg[8] = {}, db[8] = {};
-  for (uint64_t row = split; row < a.rows; row += splits) {
-    float fx[8], fd[8];
-    widen_unit(row_unit<SRC, true, false>(static_cast<const uint8_t*>(a.x[rank]) + row * src_bytes, u, full, part, H, a.gsh), fx);
-    widen_unit(row_unit<DT, true, false>(static_cast<const uint8_t*>(a.dy[rank]) + row * row_bytes, u, full, part, 0, 0), fd);
-    const float mean = as_global(a.mean[rank])[row], rstd = as_global(a.rstd[rank])[row];
+  for (int rank = 0; rank < a.ranks; ++rank)
+    for (uint64_t row = split; row < a.rows; row += splits) {
+      float fx[8], fd[8];
+      widen_unit(row_unit<SRC>(static_cast<const uint8_t*>(a.x[rank]) + row * src_bytes, u, full, part, H, a.glog), fx);
+      widen_unit(row_unit<DT>(static_cast<const uint8_t*>(a.dy[rank]) + row * row_bytes, u, full, part), fd);
+      const float mean = as_global(a.mean[rank])[row], rstd = as_global(a.rstd[rank])[row];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dg[e] += fd[e] * ((fx[e] - mean) * rstd);
-      db[e] += fd[e];
+      for (int e = 0; e < 8; ++e) {
+        dg[e] += fd[e] * ((fx[e] - mean) * rstd);
+        db[e] += fd[e];
+      }
     }
-  }
-  float* ws = a.ws + ((uint64_t)(a.rank0 + rank) * splits + split) * 2 * H;
-  put_partial<1>(ws, u, full, part, dg);
-  put_partial<1>(ws + H, u, full, part, db);
+  float* ws = a.ws + (uint64_t)split * 2 * H;
+  put_unit<kF32>(ws, u, full, part, dg);
+  put_unit<kF32>(ws + H, u, full, part, db);
 }
 
 template <int SRC, int DT, int WT>
 __global__ __launch_bounds__(1024) void ln_backward_wide_rows_kernel(LnArgs a) {
   constexpr int TPR = 1024;
-  __shared__ float red[2][TPR / kWave];
+  __shared__ float red[2][2][TPR / kWave];
   const int rank = blockIdx.y;
   const uint64_t H = a.hidden, full = H / 8, units = (H + 7) / 8, row_bytes = H * Traits<DT>::B;
   const uint64_t src_bytes = SRC == kE4M3 ? a.row_bytes : row_bytes;
   const uint32_t part = (uint32_t)(H % 8);
+  int turn = 0;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const uint8_t* x = static_cast<const uint8_t*>(a.x[rank]) + row * src_bytes;
     const uint8_t* dy = static_cast<const uint8_t*>(a.dy[rank]) + row * row_bytes;
     const float mean = as_global(a.mean[rank])[row], rstd = as_global(a.rstd[rank])[row];
-    float n[8], w[8], g[8], s1 = 0.0f, s2 = 0.0f;
+    float n[8], w[8], g[8], s[2] = {0.0f, 0.0f};
     auto unit = [&](uint64_t u) {
-      widen_unit(row_unit<SRC, true, false>(x, u, full, part, H, a.gsh), n);
-      widen_unit(row_unit<DT, true, false>(dy, u, full, part, 0, 0), w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = 1.0f;
-      if (a.gamma[rank]) widen_unit(row_unit<WT, true, false>(a.gamma[rank], u, full, part, 0, 0), g);
+      widen_unit(row_unit<SRC>(x, u, full, part, H, a.glog), n);
+      widen_unit(row_unit<DT>(dy, u, full, part), w);
+      weight_unit<WT>(a.gamma[rank], 1.0f, u, full, part, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         n[e] = (n[e] - mean) * rstd;
@@ -438,52 +552,61 @@ __global__ __launch_bounds__(1024) void ln_backward_wide_rows_kernel(LnArgs a) {
       unit(u);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s1 += w[e];
-        s2 += w[e] * n[e];
+        s[0] += w[e];
+        s[1] += w[e] * n[e];
       }
     }
-    const float c1 = row_sum<TPR>(s1, red[0]) / (float)H;
-    const float c2 = row_sum<TPR>(s2, red[1]) / (float)H;
+    row_sums<TPR, 2>(s, red[turn]);
+    turn ^= 1;
+    const float c1 = s[0] / (float)H, c2 = s[1] / (float)H;
     for (uint64_t u = threadIdx.x; u < units; u += TPR) {
       unit(u);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = rstd * (w[e] - c1 - n[e] * c2);
-      put_unit<DT, true, false>(static_cast<uint8_t*>(a.dx[rank]) + row * row_bytes, u, full, part, w);
+      put_unit<DT>(static_cast<uint8_t*>(a.dx[rank]) + row * row_bytes, u, full, part, w);
       if constexpr (SRC == kE4M3) {
         if (a.y[rank]) {
           float b[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) b[e] = 0.0f;
-          if (a.beta[rank]) widen_unit(row_unit<WT, true, false>(a.beta[rank], u, full, part, 0, 0), b);
+          weight_unit<WT>(a.beta[rank], 0.0f, u, full, part, b);
 #pragma unroll
           for (int e = 0; e < 8; ++e) n[e] = n[e] * g[e] + b[e];
-          put_unit<DT, true, false>(static_cast<uint8_t*>(a.y[rank]) + row * row_bytes, u, full, part, n);
+          put_unit<DT>(static_cast<uint8_t*>(a.y[rank]) + row * row_bytes, u, full, part, n);
         }
       }
     }
   }
 }
 
-// The weights' gradients: column j of the `parts` partial rows, added by 16
-// waves (each every 16th row, then one after the other in LDS), divided by
-// p for an average, and stored to every rank.
+// The weights' gradients: 64 columns to a workgroup, each column's `parts`
+// partial sums added by 16 waves (each every 16th, 16 loads in flight) and
+// these in order, divided by p for an average, and stored to every rank.
+// 4.9 us for 256 x 2 x 7168 (6.5 us with the loads in a plain loop, 8.5 with
+// 32 columns to a workgroup).
+constexpr int kJoinBlock = 1024, kJoinWays = kJoinBlock / kWave, kJoinLoads = 16;
+
 template <int WT>
-__global__ __launch_bounds__(1024) void ln_join_kernel(LnJoinArgs a) {
-  constexpr int NW = 1024 / kWave;
-  __shared__ float sums[NW][kWave];
-  const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const uint64_t cols = 2 * a.hidden, j = (uint64_t)blockIdx.x * kWave + lane;
+__global__ __launch_bounds__(kJoinBlock) void ln_join_kernel(LnJoinArgs a) {
+  __shared__ float sums[kJoinWays][kWave];
+  const uint32_t col = threadIdx.x % kWave, way = threadIdx.x / kWave;
+  const uint64_t cols = 2 * a.hidden, j = (uint64_t)blockIdx.x * kWave + col;
   float s = 0.0f;
   if (j < cols) {
     const float* w = as_global(a.ws) + j;
-#pragma unroll 8
-    for (uint32_t k = wave; k < a.parts; k += NW) s += w[(uint64_t)k * cols];
-  }
-  sums[wave][lane] = s;
-  __syncthreads();
-  if (wave != 0 || j >= cols) return;
+    uint32_t k = way;
+    for (; k + (kJoinLoads - 1) * kJoinWays < a.parts; k += kJoinLoads * kJoinWays) {
+      float v[kJoinLoads];
 #pragma unroll
-  for (int w = 1; w < NW; ++w) s += sums[w][lane];
+      for (int i = 0; i < kJoinLoads; ++i) v[i] = w[(uint64_t)(k + i * kJoinWays) * cols];
+#pragma unroll
+      for (int i = 0; i < kJoinLoads; ++i) s += v[i];
+    }
+    for (; k < a.parts; k += kJoinWays) s += w[(uint64_t)k * cols];
+  }
+  sums[way][col] = s;
+  __syncthreads();
+  if (way != 0 || j >= cols) return;
+#pragma unroll
+  for (int k = 1; k < kJoinWays; ++k) s += sums[k][col];
   if (a.avg) s /= (float)a.p;
   const bool beta = j >= a.hidden;
   const uint64_t c = beta ? j - a.hidden : j;
@@ -493,12 +616,14 @@ __global__ __launch_bounds__(1024) void ln_join_kernel(LnJoinArgs a) {
   }
 }
 
-// Lanes per row and units per lane for a width, 0 lanes: too wide.  Two
-// units a lane keep the backward pass (16 sums of weight gradients a unit,
-// this row and the next in registers) within half of a SIMD's registers.
+// Lanes per row and 8-element units per lane (two 16-byte units of fp32
+// each) for a width, 0 lanes: the wide kernels' (or narrower than a unit).
+// At least half of the lanes' units lie in the row, except in the narrow
+// classes of 16 and 64 lanes.  (8 x 16384 rows of 128 bf16 took 15 us forward
+// and 37 us backward with 16 lanes to a row, 32 and 64 us with 64.)
 void row_shape(uint64_t hidden, int* tpr, int* nu) {
   const uint64_t units = (hidden + 7) / 8;
-  *tpr = units <= 128 ? 64 : units <= 512 ? 256 : units <= 1024 ? 512 : units <= 2048 ? 1024 : 0;
+  *tpr = hidden < 8 ? 0 : units <= 32 ? 16 : units <= 128 ? 64 : units <= 512 ? 256 : units <= 1024 ? 512 : units <= 2048 ? 1024 : 0;
   *nu = *tpr && units <= (uint64_t)*tpr ? 1 : 2;
 }
 
@@ -509,44 +634,46 @@ int with_shape(uint64_t hidden, F f) {
   row_shape(hidden, &tpr, &nu);
   const std::integral_constant<int, 1> one;
   const std::integral_constant<int, 2> two;
+  if (tpr == 16) return nu == 1 ? f(std::integral_constant<int, 16>(), one) : f(std::integral_constant<int, 16>(), two);
   if (tpr == 64) return nu == 1 ? f(std::integral_constant<int, 64>(), one) : f(std::integral_constant<int, 64>(), two);
   if (tpr == 256) return nu == 1 ? f(std::integral_constant<int, 256>(), one) : f(std::integral_constant<int, 256>(), two);
   if (tpr == 512) return f(std::integral_constant<int, 512>(), two);
   return f(std::integral_constant<int, 1024>(), two);
 }
 
-template <int DT, int WT>
-int forward_t(const LnArgs& a, int ranks, bool ckpt, hipStream_t s) {
+bool is_wide(const LnArgs& a) {
   int tpr, nu;
   row_shape(a.hidden, &tpr, &nu);
-  const bool tail = a.hidden % 8 != 0;
-  if (!tpr) {
-    const uint32_t gx = (uint32_t)(a.rows < 65536 ? a.rows : 65536);
-    if (ckpt) hipLaunchKernelGGL((ln_forward_wide_kernel<DT, WT, true>), dim3(gx, ranks), dim3(1024), 0, s, a);
-    else hipLaunchKernelGGL((ln_forward_wide_kernel<DT, WT, false>), dim3(gx, ranks), dim3(1024), 0, s, a);
+  return !tpr;
+}
+
+template <int DT, int WT>
+int forward_t(const LnArgs& a, bool ckpt, hipStream_t s) {
+  if (is_wide(a)) {
+    const dim3 grid((uint32_t)std::min<uint64_t>(a.rows, 65536), a.ranks), block(1024);
+    if (ckpt) hipLaunchKernelGGL((ln_forward_wide_kernel<DT, WT, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((ln_forward_wide_kernel<DT, WT, false>), grid, block, 0, s, a);
     return (int)hipGetLastError();
   }
   return with_shape(a.hidden, [&](auto T, auto N) {
-    constexpr int TPR = decltype(T)::value, NU = decltype(N)::value, RPB = block_of(TPR) / TPR;
-    const uint64_t need = (a.rows + RPB - 1) / RPB;
-    const uint64_t cap = ln_forward_groups(ranks, TPR);
-    const dim3 grid((uint32_t)(need < cap ? need : cap), ranks), block(block_of(TPR));
-    if (ckpt) hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, false, true>), grid, block, 0, s, a);
-    else if (tail) hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, true, false>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, false, false>), grid, block, 0, s, a);
+    constexpr int TPR = decltype(T)::value, NU = decltype(N)::value * 8 / kElems<DT>, RUN = block_of(TPR) / TPR * kRows;
+    const uint64_t runs = (a.rows + RUN - 1) / RUN;
+    if (runs > 0x7fffffffull) return (int)hipErrorInvalidConfiguration;
+    const dim3 grid((uint32_t)runs, a.ranks), block(block_of(TPR));
+    constexpr bool PACKED = TPR < kWave;  // several rows to a wave
+    if (ckpt) hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, PACKED, true>), grid, block, 0, s, a);
+    else if (PACKED || a.hidden % kElems<DT>) hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, true, false>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, PACKED, false>), grid, block, 0, s, a);
     return (int)hipGetLastError();
   });
 }
 
 template <int DT, int WT>
-int backward_t(const LnArgs& a, int ranks, uint32_t groups, bool ckpt, hipStream_t s) {
-  int tpr, nu;
-  row_shape(a.hidden, &tpr, &nu);
-  const bool tail = a.hidden % 8 != 0;
-  if (!tpr) {
+int backward_t(const LnArgs& a, uint32_t groups, bool ckpt, hipStream_t s) {
+  if (is_wide(a)) {
     const uint64_t chunks = ((a.hidden + 7) / 8 + kBlock - 1) / kBlock;
     if (chunks * groups > 0x7fffffffull) return (int)hipErrorInvalidConfiguration;
-    const dim3 cols((uint32_t)(chunks * groups), ranks), rows((uint32_t)(a.rows < 65536 ? a.rows : 65536), ranks);
+    const dim3 cols((uint32_t)(chunks * groups)), rows((uint32_t)std::min<uint64_t>(a.rows, 65536), a.ranks);
     if (ckpt) {
       hipLaunchKernelGGL((ln_backward_wide_columns_kernel<kE4M3, DT>), cols, dim3(kBlock), 0, s, a, groups);
       hipLaunchKernelGGL((ln_backward_wide_rows_kernel<kE4M3, DT, WT>), rows, dim3(1024), 0, s, a);
@@ -557,54 +684,57 @@ int backward_t(const LnArgs& a, int ranks, uint32_t groups, bool ckpt, hipStream
     return (int)hipGetLastError();
   }
   return with_shape(a.hidden, [&](auto T, auto N) {
-    constexpr int TPR = decltype(T)::value, NU = decltype(N)::value;
-    const dim3 grid(groups, ranks), block(block_of(TPR));
-    if (ckpt) hipLaunchKernelGGL((ln_backward_kernel<kE4M3, DT, WT, TPR, NU, false>), grid, block, 0, s, a);
-    else if (tail) hipLaunchKernelGGL((ln_backward_kernel<DT, DT, WT, TPR, NU, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((ln_backward_kernel<DT, DT, WT, TPR, NU, false>), grid, block, 0, s, a);
+    constexpr int TPR = decltype(T)::value, NU = decltype(N)::value * 8 / kElems<DT>;
+    const dim3 grid(groups), block(block_of(TPR));
+    constexpr bool PACKED = TPR < kWave;
+    if (ckpt) hipLaunchKernelGGL((ln_backward_kernel<kE4M3, DT, WT, TPR, NU, PACKED>), grid, block, 0, s, a);
+    else if (PACKED || a.hidden % kElems<DT>) hipLaunchKernelGGL((ln_backward_kernel<DT, DT, WT, TPR, NU, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((ln_backward_kernel<DT, DT, WT, TPR, NU, PACKED>), grid, block, 0, s, a);
     return (int)hipGetLastError();
   });
 }
 
 }  // namespace
 
-// Workgroups per rank of the forward pass.
-uint32_t ln_forward_groups(int ranks, int tpr) {
-  const uint32_t total = tpr == 1024 ? 512 : 2048;
-  const uint32_t g = total / (uint32_t)ranks;
-  return g ? g : 1;
-}
-
-// Workgroups per rank of the backward pass: by the shape alone (results and
-// workspace must not depend on the device or on the grid limit).  Two
-// 256-lane workgroups fit a CU's registers, one of 1024 lanes.
+// Workgroups of a launch of the backward pass: by the shape alone (results
+// and workspace must not depend on the device or on the grid limit).  One
+// workgroup of 512 lanes to a CU: 8 x 4096 x 7168 bf16 took 238 us with 256,
+// 252 with 512 and 279 with 384, whose second round is short.  Two of 256
+// lanes: 3 x 1777 x 2565 fp32 took 40 us with 512, 43.5 with 384, 45 and 48
+// with 768 and 1024, which write more partial sums.
 uint32_t ln_backward_groups(int p, uint64_t rows, uint64_t hidden) {
   int tpr, nu;
   row_shape(hidden, &tpr, &nu);
-  const uint64_t rpb = tpr == 64 ? 4 : 1, need = (rows + rpb - 1) / rpb;
-  uint64_t g = (tpr == 1024 || tpr == 0 ? 256 : 512) / (uint64_t)p;
-  if (g < 1) g = 1;
-  return (uint32_t)(need < g ? (need ? need : 1) : g);
+  const uint64_t rpb = tpr && tpr < kBlock ? kBlock / tpr : 1, all = rows * (uint64_t)std::min(p, kArgRanks), need = (all + rpb - 1) / rpb;
+  const uint64_t most = tpr && tpr <= kBlock ? 512 : 256;
+  return (uint32_t)std::max<uint64_t>(1, std::min(need, most));
 }
 
-int launch_ln_forward(int dtype, int wdtype, const LnArgs& a, int ranks, bool ckpt, void* stream) {
-  hipStream_t s = (hipStream_t)stream;
-  if (dtype == kF32) return forward_t<kF32, kF32>(a, ranks, ckpt, s);
-  return wdtype == kF32 ? forward_t<kBF16, kF32>(a, ranks, ckpt, s) : forward_t<kBF16, kBF16>(a, ranks, ckpt, s);
+// Whether the forward kernel of a width writes checkpoints of such groups:
+// a group's lanes must lie in one run of a row's.
+bool ln_forward_keeps(int dtype, uint64_t hidden, uint64_t group) {
+  int tpr, nu;
+  row_shape(hidden, &tpr, &nu);
+  return group <= (uint64_t)(tpr == 0 ? 512 : std::min(tpr, kWave) * (dtype == kF32 ? 4 : 8));
 }
 
-int launch_ln_backward(int dtype, int wdtype, const LnArgs& a, int ranks, uint32_t groups, bool ckpt, void* stream) {
+int launch_ln_forward(int dtype, int wdtype, const LnArgs& a, bool ckpt, void* stream) {
   hipStream_t s = (hipStream_t)stream;
-  if (dtype == kF32) return backward_t<kF32, kF32>(a, ranks, groups, ckpt, s);
-  return wdtype == kF32 ? backward_t<kBF16, kF32>(a, ranks, groups, ckpt, s)
-                        : backward_t<kBF16, kBF16>(a, ranks, groups, ckpt, s);
+  if (dtype == kF32) return forward_t<kF32, kF32>(a, ckpt, s);
+  return wdtype == kF32 ? forward_t<kBF16, kF32>(a, ckpt, s) : forward_t<kBF16, kBF16>(a, ckpt, s);
+}
+
+int launch_ln_backward(int dtype, int wdtype, const LnArgs& a, uint32_t groups, bool ckpt, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  if (dtype == kF32) return backward_t<kF32, kF32>(a, groups, ckpt, s);
+  return wdtype == kF32 ? backward_t<kBF16, kF32>(a, groups, ckpt, s) : backward_t<kBF16, kBF16>(a, groups, ckpt, s);
 }
 
 int launch_ln_join(int wdtype, const LnJoinArgs& a, void* stream) {
   hipStream_t s = (hipStream_t)stream;
-  const uint64_t blocks = (2 * a.hidden + kWave - 1) / kWave;
-  if (wdtype == kF32) hipLaunchKernelGGL((ln_join_kernel<kF32>), dim3((uint32_t)blocks), dim3(1024), 0, s, a);
-  else hipLaunchKernelGGL((ln_join_kernel<kBF16>), dim3((uint32_t)blocks), dim3(1024), 0, s, a);
+  const dim3 grid((uint32_t)((2 * a.hidden + kWave - 1) / kWave)), block(kJoinBlock);
+  if (wdtype == kF32) hipLaunchKernelGGL((ln_join_kernel<kF32>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((ln_join_kernel<kBF16>), grid, block, 0, s, a);
   return (int)hipGetLastError();
 }
 

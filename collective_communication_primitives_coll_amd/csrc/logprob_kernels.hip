@@ -38,8 +38,8 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 constexpr float kFar = -16384.0f;
-constexpr int kChunk = 4;                          // units per lane and step
-constexpr uint32_t kChunkUnits = kChunk * kWave;   // units of a step of the wave
+constexpr int kStep = 32;                          // elements per lane and step
+constexpr int64_t kWaveStep = (int64_t)kStep * kWave;
 
 // The order of fp32 values as unsigned integers (both zeros alike).
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -108,11 +108,11 @@ __device__ __forceinline__ unsigned long long key_of(float v, uint32_t index) {
 struct Piece {
   int64_t begin;       // first element
   uint32_t head, tail; // elements
-  uint32_t units;
+  uint32_t units;      // of 16 bytes
 };
 template <int DT>
 __device__ __forceinline__ Piece piece_of(const uint8_t* row, int64_t vocab, int64_t len, int k) {
-  constexpr int B = Traits<DT>::B;
+  constexpr int B = Traits<DT>::B, E = kElems<DT>;
   const int64_t mis = (int64_t)((uintptr_t)row & 15) / B;
   Piece c;
   c.begin = k ? (int64_t)k * len - mis : 0;
@@ -122,18 +122,15 @@ __device__ __forceinline__ Piece piece_of(const uint8_t* row, int64_t vocab, int
   const uint32_t n = (uint32_t)(end - c.begin);
   const uint32_t h = (uint32_t)(((16 - (((uintptr_t)row + c.begin * B) & 15)) & 15) / B);
   c.head = h < n ? h : n;
-  c.units = (n - c.head) / 8;
-  c.tail = n - c.head - c.units * 8;
+  c.units = (n - c.head) / E;
+  c.tail = n - c.head - c.units * E;
   return c;
 }
 
 template <int DT>
-__device__ __forceinline__ RawUnit<DT> masked_unit() {
-  RawUnit<DT> r;
-#pragma unroll
-  for (auto& v : r.v) v = DT == kBF16 ? u32x4{0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}
-                                      : u32x4{0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u};
-  return r;
+__device__ __forceinline__ RawUnit<DT, kElems<DT>> masked_unit() {
+  const uint32_t w = DT == kBF16 ? 0xff80ff80u : 0xff800000u;
+  return RawUnit<DT, kElems<DT>>{{u32x4{w, w, w, w}}};
 }
 
 // A lane's running maximum m (raw), S = sum 2^d and A = sum 2^d d about it.
@@ -155,7 +152,8 @@ struct Running {
 
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
-  constexpr int B = Traits<DT>::B;
+  constexpr int B = Traits<DT>::B, E = kElems<DT>, kChunk = kStep / E;
+  constexpr uint32_t kChunkUnits = kChunk * kWave;
   const uint32_t lane = threadIdx.x % kWave;
   const float c = a.scale * kLog2e;
   const uint64_t items = a.rows * (uint64_t)a.plan.pieces, step = (uint64_t)gridDim.x * (kBlock / kWave);
@@ -173,12 +171,12 @@ __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
 
     Running run;
     TopList list;
-    RawUnit<DT> cur[kChunk], nxt[kChunk];
-    auto load = [&](RawUnit<DT> (&to)[kChunk], uint32_t u0) {
+    RawUnit<DT, E> cur[kChunk], nxt[kChunk];
+    auto load = [&](RawUnit<DT, E> (&to)[kChunk], uint32_t u0) {
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) {
         const uint32_t u = u0 + i * kWave + lane;
-        to[i] = u < pc.units ? load_unit<DT, true>(units, u) : masked_unit<DT>();
+        to[i] = u < pc.units ? load_unit<DT, E, true>(units, u * E) : masked_unit<DT>();
       }
     };
     if (pc.units) load(cur, 0);
@@ -186,24 +184,24 @@ __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
     float end = -__builtin_inff();
     uint32_t end_off = ~0u;
     if (lane < pc.head) end_off = lane;
-    else if (lane >= 8 && lane - 8 < pc.tail) end_off = pc.head + pc.units * 8 + lane - 8;
+    else if (lane >= 8 && lane - 8 < pc.tail) end_off = pc.head + pc.units * E + lane - 8;
     using S = typename Traits<DT>::S;
     if (end_off != ~0u) end = widen1<DT>(reinterpret_cast<const S*>(base)[pc.begin + end_off]);
     // the target's logit, where it lies in this piece
     const int64_t t_off = as_global(a.targets)[row] - a.first_index[r] - pc.begin;
     float z = -__builtin_inff();
-    if (t_off >= 0 && t_off < (int64_t)(pc.head + pc.units * 8 + pc.tail))
+    if (t_off >= 0 && t_off < (int64_t)(pc.head + pc.units * E + pc.tail))
       z = widen1<DT>(reinterpret_cast<const S*>(base)[pc.begin + t_off]);
     for (uint32_t u0 = 0; u0 < pc.units; u0 += kChunkUnits) {
       const bool more = u0 + kChunkUnits < pc.units;
       if (more) load(nxt, u0 + kChunkUnits);
-      float f[kChunk][8], um[kChunk], top = -FLT_MAX;
+      float f[kChunk][E], um[kChunk], top = -FLT_MAX;
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) {
         widen_unit(cur[i], f[i]);
         um[i] = f[i][0];
 #pragma unroll
-        for (int e = 1; e < 8; ++e) um[i] = fmaxf(um[i], f[i][e]);
+        for (int e = 1; e < E; ++e) um[i] = fmaxf(um[i], f[i][e]);
         top = fmaxf(top, um[i]);
       }
       run.rebase(fmaxf(run.m, top), c);
@@ -211,7 +209,7 @@ __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < E; ++e) {
           const float d = (f[i][e] - run.m) * c, x = __builtin_amdgcn_exp2f(d);
           s[i] += x;
           w[i] += x * fmaxf(d, kFar);
@@ -234,8 +232,8 @@ __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
           if (!__any(order_of(um[i]) > (uint32_t)(list.bar >> 32))) continue;
           const uint32_t u = u0 + i * kWave + lane;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            list.offer(u < pc.units ? key_of(f[i][e], index0 + pc.head + u * 8 + e) : 0, a.top);
+          for (int e = 0; e < E; ++e)
+            list.offer(u < pc.units ? key_of(f[i][e], index0 + pc.head + u * E + e) : 0, a.top);
         }
       }
       if (more) {
@@ -342,7 +340,7 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinInput a, Logpr
 
 // Gradient.  A wave takes kGradLen elements of one row's shard, cut as the
 // forward pass's pieces.
-constexpr int64_t kGradLen = (int64_t)kChunkUnits * 8;
+constexpr int64_t kGradLen = kWaveStep;
 
 struct GradRow {
   float m, shift, gl, gh, h, scale, c;
@@ -357,7 +355,7 @@ struct GradRow {
 
 template <int DT>
 __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(LogprobGradArgs a, LogprobPlan plan) {
-  constexpr int B = Traits<DT>::B;
+  constexpr int B = Traits<DT>::B, E = kElems<DT>, kChunk = kStep / E;
   const uint32_t lane = threadIdx.x % kWave;
   const uint64_t items = a.rows * (uint64_t)plan.pieces, step = (uint64_t)gridDim.x * (kBlock / kWave);
   uint64_t item = (uint64_t)blockIdx.x * (kBlock / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -372,15 +370,15 @@ __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(LogprobGradArgs a,
     const Piece pc = piece_of<DT>(base, vocab, kGradLen, piece - plan.first[r]);
     const uint8_t* units = base + (pc.begin + pc.head) * B;
     uint8_t* outs = out + (pc.begin + pc.head) * B;
-    RawUnit<DT> x[kChunk];
+    RawUnit<DT, E> x[kChunk];
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
       const uint32_t u = i * kWave + lane;
-      x[i] = u < pc.units ? load_unit<DT, true>(units, u) : masked_unit<DT>();
+      x[i] = u < pc.units ? load_unit<DT, E, true>(units, u * E) : masked_unit<DT>();
     }
     uint32_t end_off = ~0u;
     if (lane < pc.head) end_off = lane;
-    else if (lane >= 8 && lane - 8 < pc.tail) end_off = pc.head + pc.units * 8 + lane - 8;
+    else if (lane >= 8 && lane - 8 < pc.tail) end_off = pc.head + pc.units * E + lane - 8;
     float end = 0.0f;
     if (end_off != ~0u)
       end = widen1<DT>(reinterpret_cast<const typename Traits<DT>::S*>(base)[pc.begin + end_off]);
@@ -407,24 +405,24 @@ __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(LogprobGradArgs a,
     const float own = g.gl * a.scale;
     // the target's place from the piece's first element, if it is here
     const int64_t t_off = counts ? target - a.first_index[r] - pc.begin : -1;
-    const uint32_t n = pc.head + pc.units * 8 + pc.tail;
+    const uint32_t n = pc.head + pc.units * E + pc.tail;
     const uint32_t t = t_off >= 0 && t_off < (int64_t)n ? (uint32_t)t_off : ~0u;
-    const uint32_t t_unit = t == ~0u || t < pc.head ? ~0u : (t - pc.head) / 8;
+    const uint32_t t_unit = t == ~0u || t < pc.head ? ~0u : (t - pc.head) / E;
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) {
       const uint32_t u = i * kWave + lane;
       if (u >= pc.units) continue;
-      float f[8];
+      float f[E];
       widen_unit(x[i], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = g(f[e]);
+      for (int e = 0; e < E; ++e) f[e] = g(f[e]);
       if (u == t_unit) {
-        const uint32_t te = (t - pc.head) % 8;
+        const uint32_t te = (t - pc.head) % E;
 #pragma unroll
-        for (uint32_t e = 0; e < 8; ++e)
+        for (uint32_t e = 0; e < E; ++e)
           if (e == te) f[e] += own;
       }
-      store_unit<DT, true>(outs, u, narrow_unit<DT>(f));
+      store_unit<DT, E, true>(outs, u * E, narrow_unit<DT, E>(f));
     }
     if (end_off != ~0u) {
       float v = g(end);
@@ -445,11 +443,11 @@ int pieces_of(int64_t vocab, int64_t len) { return vocab ? (int)((vocab + 7 + le
 
 }  // namespace
 
-// Pieces of a step (kChunkUnits units) or more: enough for some 8192 waves
+// Pieces of a wave's step or more: enough for some 8192 waves
 // over all rows, and none over 32768 elements, as far as a row's 64 pieces
 // allow.
 void logprob_plan(int p, uint64_t rows, const int64_t* vocab, LogprobPlan* plan) {
-  const int64_t unit = (int64_t)kChunkUnits * 8, most = kMaxPieces / p;
+  const int64_t unit = kWaveStep, most = kMaxPieces / p;
   const uint64_t want = rows ? (8192 + rows * (uint64_t)p - 1) / (rows * (uint64_t)p) : 1;
   plan->first[0] = 0;
   for (int r = 0; r < p; ++r) {
