@@ -623,7 +623,7 @@ __global__ __launch_bounds__(kJoinBlock) void ln_join_kernel(LnJoinArgs a) {
 // and 37 us backward with 16 lanes to a row, 32 and 64 us with 64.)
 void row_shape(uint64_t hidden, int* tpr, int* nu) {
   const uint64_t units = (hidden + 7) / 8;
-  *tpr = hidden < 8 ? 0 : units <= 32 ? 16 : units <= 128 ? 64 : units <= 512 ? 256 : units <= 1024 ? 512 : units <= 2048 ? 1024 : 0;
+  *tpr = hidden < 8 ? 0 : units <= 32 ? 16 : units <= 128 ? 64 : units <= 512 ? 256 : units <= 768 ? 384 : units <= 1024 ? 512 : units <= 1536 ? 768 : units <= 2048 ? 1024 : 0;
   *nu = *tpr && units <= (uint64_t)*tpr ? 1 : 2;
 }
 
@@ -637,7 +637,9 @@ int with_shape(uint64_t hidden, F f) {
   if (tpr == 16) return nu == 1 ? f(std::integral_constant<int, 16>(), one) : f(std::integral_constant<int, 16>(), two);
   if (tpr == 64) return nu == 1 ? f(std::integral_constant<int, 64>(), one) : f(std::integral_constant<int, 64>(), two);
   if (tpr == 256) return nu == 1 ? f(std::integral_constant<int, 256>(), one) : f(std::integral_constant<int, 256>(), two);
+  if (tpr == 384) return f(std::integral_constant<int, 384>(), two);
   if (tpr == 512) return f(std::integral_constant<int, 512>(), two);
+  if (tpr == 768) return f(std::integral_constant<int, 768>(), two);
   return f(std::integral_constant<int, 1024>(), two);
 }
 
