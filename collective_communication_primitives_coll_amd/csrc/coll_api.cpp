@@ -1819,7 +1819,7 @@ COLL_EXPORT size_t coll_vocab_logprob_workspace_bytes(int p, size_t rows, const 
   coll::LogprobPlan plan;
   coll::logprob_plan(p, rows, vocab, &plan);
   size_t bytes;
-  return mul_ok(rows, (size_t)plan.pieces, 16 + 8 * (size_t)top_k, &bytes) ? bytes : 0;
+  return mul_ok(rows, (size_t)plan.pieces, coll::logprob_piece_bytes(plan, top_k), &bytes) ? bytes : 0;
 }
 
 COLL_EXPORT coll_status_t coll_vocab_logprob(const void* const* logits, const int64_t* ld, const int64_t* vocab,
@@ -1843,7 +1843,7 @@ COLL_EXPORT coll_status_t coll_vocab_logprob(const void* const* logits, const in
     return COLL_ERR_INVALID_ARG;
   coll::logprob_plan(p, rows, vocab, &a.plan);
   size_t need;
-  if (!mul_ok(rows, (size_t)a.plan.pieces, 16 + 8 * (size_t)top_k, &need)) return COLL_ERR_INVALID_ARG;
+  if (!mul_ok(rows, (size_t)a.plan.pieces, coll::logprob_piece_bytes(a.plan, top_k), &need)) return COLL_ERR_INVALID_ARG;
   if (!workspace || !elem_aligned1(workspace, 16) || workspace_bytes < need) return COLL_ERR_INVALID_ARG;
   RangeSet rs;
   for (int r = 0; r < p; ++r) rs.add(logits[r], shard_bytes(rows, ld[r], vocab[r], d), false);
@@ -1872,7 +1872,8 @@ COLL_EXPORT coll_status_t coll_vocab_logprob(const void* const* logits, const in
   }
   a.targets = targets;
   a.part = (float*)workspace;
-  a.keys = (unsigned long long*)((char*)workspace + rows * (size_t)a.plan.pieces * 16);
+  a.places = (uint32_t*)((char*)workspace + rows * (size_t)a.plan.pieces * 16);
+  a.bests = (float*)((char*)workspace + rows * (size_t)a.plan.pieces * 32);
   a.rows = rows;
   a.scale = inv_temp;
   a.p = p;

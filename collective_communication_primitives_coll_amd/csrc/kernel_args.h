@@ -221,8 +221,14 @@ struct Ckpt8Args {
 // segs[rank] pieces; all pieces of a row number at most kMaxPieces (a wave).
 constexpr int kMaxPieces = 64;
 constexpr int kMaxTop = 32;
+// Elements that a wave takes in one step.
+constexpr int kLogprobStep = 2048;
+// Groups of elements (a row's) whose largest the search for alternatives
+// starts from.  Eight lanes, so whole 128-byte lines, share a group.
+constexpr int kMaxGroups = 1024, kGroupLanes = 8, kSegGroups = 64 / kGroupLanes;
 struct LogprobPlan {
   int pieces;                    // per row, over all ranks
+  int segs, seg_steps;           // a piece's segments, of kSegGroups groups each, and the steps of one
   int first[kMaxRanks + 1];      // first piece of each rank, and the end
   int64_t len[kMaxRanks];        // elements per piece (the rank's last may be shorter)
 };
@@ -233,7 +239,8 @@ struct LogprobArgs {
   LogprobPlan plan;
   const int64_t* targets;
   float* part;                   // [rows][pieces][4]: max, sum, entropy sum, target's logit (-inf where elsewhere)
-  unsigned long long* keys;      // [rows][pieces][top]
+  uint32_t* places;              // with alternatives: [rows][pieces][4], where each piece lies
+  float* bests;                  // with alternatives: [rows][pieces][segs][kSegGroups], largest elements
   uint64_t rows;
   float scale;                   // inverse temperature
   int p;
@@ -367,6 +374,10 @@ int launch_ckpt8(int kind, int dtype, Ckpt8Args a, int ranks, void* stream);
 
 // Vocabulary log probabilities: the pieces' pass and the join over them,
 // then the logits' gradient.
+// Workspace bytes of a piece.
+inline size_t logprob_piece_bytes(const LogprobPlan& plan, int top) {
+  return top ? 32 + (size_t)plan.segs * kSegGroups * 4 : 16;
+}
 void logprob_plan(int p, uint64_t rows, const int64_t* vocab, LogprobPlan* plan);
 int launch_logprob(int dtype, const LogprobArgs& a, const LogprobJoinArgs& j, void* stream);
 int launch_logprob_backward(int dtype, const LogprobGradArgs& a, void* stream);

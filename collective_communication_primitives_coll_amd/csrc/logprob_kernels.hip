@@ -15,8 +15,19 @@
 // keeps its own running maximum and its sums about it (one rescale per
 // chunk of 32 elements), and the lanes meet once, at the piece's end.
 // The join kernel, a wave to a row and a lane to a piece, does what
-// the AllReduce of maxima and sums over the ranks would, and stores the
-// results to every rank.
+// the AllReduce of maxima and sums over the ranks would, finds the
+// alternatives, and stores the results to every rank.
+//
+// Alternatives.  A piece also writes down the largest element of each group
+// of eight lanes and a step (or a few, so that a row has 1024 groups at
+// most), which costs little beside the running maximum.  64 lanes' shares of
+// a row's groups bound its k best elements from below by the k-th largest of
+// theirs, and few groups reach the bound: the join wave reads those again,
+// whole 128-byte lines, and ranks the elements that reach it by counting.
+// 2048 rows of 131072 bf16: 89 us without alternatives, ZZ us with 8.
+// (Insertion into a sorted list while the chunks came took 120 us; a search
+// in each piece, whose end no other work hides, 127 us; groups of one lane's
+// elements over a whole piece, each in a line of its own, 110 us.)
 //
 // Sums run in base 2 (v_exp_f32), in fp32.  Differences to the maximum are
 // taken before the scaling, so large logits lose nothing, and are held at
@@ -38,8 +49,10 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 constexpr float kFar = -16384.0f;
-constexpr int kStep = 32;                          // elements per lane and step
-constexpr int64_t kWaveStep = (int64_t)kStep * kWave;
+// Where the sums take one fma an element for its difference to the maximum:
+// eps, at most 2^-25 of m c, is then small enough to be taken back out.
+constexpr float kPlainMax = 1e4f, kPlainScale = 100.0f;
+constexpr int kStep = kLogprobStep / kWave;  // elements per lane and step
 
 // The order of fp32 values as unsigned integers (both zeros alike).
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -50,27 +63,20 @@ __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
 
-// The `top` largest of a wave's elements, one per lane in descending order:
-// key = order of the value above the complement of the index, so that the
-// lower index wins a tie.  An empty place is 0, below every key.  bar: no key
-// at or below it can enter.
-struct TopList {
-  unsigned long long key = 0, bar = 0;
+constexpr uint32_t kMaskedOrder = 0x007fffffu;  // of -infinity
 
-  // A starting bar that at least `top` of the lanes' largest elements pass:
-  // the largest order with that many lanes at or above it, found bit by bit.
-  __device__ __forceinline__ void raise(uint32_t lane_best, int top) {
-    uint32_t t = 0;
-    for (int b = 31; b >= 0; --b) {
-      const uint32_t c = t | (1u << b);
-      const int n = __popcll(__ballot(lane_best >= c));
-      if (n >= top) {
-        t = c;
-        if (n == top) break;
-      }
-    }
-    if (t) bar = ((unsigned long long)t << 32) - 1;
-  }
+// Keys of alternatives: the order of the value above the complement of the
+// index, so that the larger key is the better entry and the lower index wins
+// a tie.
+__device__ __forceinline__ unsigned long long key_of(float v, uint32_t index) {
+  return ((unsigned long long)order_of(v) << 32) | (uint32_t)~index;
+}
+
+// The `top` largest unmasked elements of a wave, one per lane in descending
+// order, built by insertion.  An empty place is 0, below every key.  bar: no
+// key at or below it can enter.
+struct TopList {
+  unsigned long long key = 0, bar = ((unsigned long long)kMaskedOrder << 32) | 0xffffffffu;
 
   __device__ __forceinline__ void insert(unsigned long long k, int top) {
     const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(-1, (int)(uint32_t)key, 0x138 /* wave_shr:1 */, 0xf, 0xf, false);
@@ -79,6 +85,27 @@ struct TopList {
     key = key > k ? key : before > k ? k : before;
     const unsigned long long last = lane_value(key, top - 1);
     if (last > bar) bar = last;
+  }
+
+  // A lane's E elements, the first at vocabulary index `index` (`in`: the
+  // lane has any), and the largest of them: each round offers every lane's
+  // best and takes it out (NaN, which no comparison finds), until none can
+  // enter.
+  template <int E>
+  __device__ __forceinline__ void consider(float (&f)[E], float best, uint32_t index, bool in, int top) {
+    while (true) {
+      uint32_t e0 = 0;
+#pragma unroll
+      for (int e = E - 1; e >= 0; --e) e0 = f[e] == best ? (uint32_t)e : e0;
+      const unsigned long long k = in && best == best ? key_of(best, index + e0) : 0;
+      if (!__any(k > bar)) break;
+      offer(k, top);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = e0 == (uint32_t)e ? __uint_as_float(0x7fc00000u) : f[e];
+      best = f[0];
+#pragma unroll
+      for (int e = 1; e < E; ++e) best = fmaxf(best, f[e]);
+    }
   }
 
   // Every lane offers one key (0: none).
@@ -97,10 +124,6 @@ struct TopList {
     return ((unsigned long long)hi << 32) | lo;
   }
 };
-
-__device__ __forceinline__ unsigned long long key_of(float v, uint32_t index) {
-  return ((unsigned long long)order_of(v) << 32) | (uint32_t)~index;
-}
 
 // A piece of a row's shard: its elements before the first 16-byte boundary,
 // its whole units and the rest.  Pieces after the first start on such a
@@ -150,6 +173,57 @@ struct Running {
   }
 };
 
+template <int N>
+__device__ __forceinline__ float largest(const float (&f)[N]) {
+  float v = f[0];
+#pragma unroll
+  for (int e = 1; e < N; ++e) v = fmaxf(v, f[e]);
+  return v;
+}
+
+// A bound that at least `top` lanes reach (or that all unmasked elements do).
+__device__ __forceinline__ float bar_of(float mine, int top) {
+  int reached = 0;
+#pragma unroll 8
+  for (int j = 0; j < kWave; ++j) reached += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j)) >= mine;
+  return fmaxf(wave_max(reached >= top ? mine : -FLT_MAX), -FLT_MAX);
+}
+
+// LDS is written and read by one wave alone.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Entries that a wave collects in LDS; n counts also those past its end.
+template <class T, uint32_t MOST>
+struct Bag {
+  T* at;
+  uint32_t n = 0;
+  __device__ __forceinline__ void push(T v, bool in) {
+    const unsigned long long mask = __ballot(in);
+    if (!mask) return;
+    const uint32_t i = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+    if (in && i < MOST) at[i] = v;
+    n += (uint32_t)__popcll(mask);
+  }
+  __device__ __forceinline__ bool full() const { return n > MOST; }
+};
+constexpr uint32_t kBagMost = 256;
+struct JoinStore {
+  unsigned long long keys[kBagMost];
+  uint32_t groups[kBagMost];
+  unsigned long long sorted[kMaxTop];
+};
+
+template <int N>
+__device__ __forceinline__ float sum_of(const float (&v)[N]) {
+  float s = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) s += v[i];
+  return s;
+}
+
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
   constexpr int B = Traits<DT>::B, E = kElems<DT>, kChunk = kStep / E;
@@ -170,7 +244,19 @@ __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
     const uint32_t index0 = (uint32_t)(a.first_index[r] + pc.begin);  // vocabulary index of the piece's first element
 
     Running run;
-    TopList list;
+    // the largest of the lane's elements in this segment
+    float best = -__builtin_inff();
+    float* bests = as_global(a.bests) + item * (uint64_t)(a.plan.segs * kSegGroups) + lane / kGroupLanes;
+    int seg = 0, left = a.plan.seg_steps;
+    auto note = [&] {
+      best = wave_max<kGroupLanes>(best);
+      if (lane % kGroupLanes == 0) bests[seg * kSegGroups] = best;
+      best = -__builtin_inff();
+      ++seg;
+      left = a.plan.seg_steps;
+    };
+    // whether the cheap form of the sums holds so far: no masked entries
+    bool plain = c < kPlainScale;
     RawUnit<DT, E> cur[kChunk], nxt[kChunk];
     auto load = [&](RawUnit<DT, E> (&to)[kChunk], uint32_t u0) {
 #pragma unroll
@@ -195,46 +281,53 @@ __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
     for (uint32_t u0 = 0; u0 < pc.units; u0 += kChunkUnits) {
       const bool more = u0 + kChunkUnits < pc.units;
       if (more) load(nxt, u0 + kChunkUnits);
-      float f[kChunk][E], um[kChunk], top = -FLT_MAX;
+      float f[kChunk][E], top = -__builtin_inff();
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) {
         widen_unit(cur[i], f[i]);
-        um[i] = f[i][0];
-#pragma unroll
-        for (int e = 1; e < E; ++e) um[i] = fmaxf(um[i], f[i][e]);
-        top = fmaxf(top, um[i]);
+        top = fmaxf(top, largest(f[i]));
       }
       run.rebase(fmaxf(run.m, top), c);
-      float s[kChunk] = {}, w[kChunk] = {};
+      float s[kChunk] = {}, w[kChunk] = {}, ds, dw;
+      if (plain && __all(fabsf(run.m) < kPlainMax)) {
+        // one fma an element: d = z c - M for the rounded M = m c, which is
+        // off the true difference by the exactly known eps
+        const float M = run.m * c, eps = __builtin_fmaf(run.m, c, -M);
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i)
+        for (int i = 0; i < kChunk; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float d = (f[i][e] - run.m) * c, x = __builtin_amdgcn_exp2f(d);
-          s[i] += x;
-          w[i] += x * fmaxf(d, kFar);
-        }
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) {
-        run.s += s[i];
-        run.a += w[i];
+          for (int e = 0; e < E; ++e) {
+            const float d = __builtin_fmaf(f[i][e], c, -M), x = __builtin_amdgcn_exp2f(d);
+            s[i] += x;
+            w[i] = __builtin_fmaf(x, d, w[i]);
+          }
+        const float k = __builtin_amdgcn_exp2f(-eps);
+        ds = sum_of(s) * k;
+        dw = sum_of(w) * k - eps * ds;
+        // a masked entry (0 * inf) or a NaN shows here
+        plain = __all(dw == dw);
+      } else {
+        plain = false;
       }
-      if constexpr (TOP) {
-        if (u0 == 0) {
-          float best = um[0];
-#pragma unroll
-          for (int i = 1; i < kChunk; ++i) best = fmaxf(best, um[i]);
-          list.raise(order_of(best), a.top);
-        }
+      if (!plain) {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) {
-          // later units hold higher indices, so a tie with the bar loses
-          if (!__any(order_of(um[i]) > (uint32_t)(list.bar >> 32))) continue;
-          const uint32_t u = u0 + i * kWave + lane;
+          s[i] = w[i] = 0.0f;
 #pragma unroll
-          for (int e = 0; e < E; ++e)
-            list.offer(u < pc.units ? key_of(f[i][e], index0 + pc.head + u * E + e) : 0, a.top);
+          for (int e = 0; e < E; ++e) {
+            const float d = (f[i][e] - run.m) * c, x = __builtin_amdgcn_exp2f(d);
+            s[i] += x;
+            w[i] += x * fmaxf(d, kFar);
+          }
         }
+        ds = sum_of(s);
+        dw = sum_of(w);
+      }
+      run.s += ds;
+      run.a += dw;
+      if constexpr (TOP) {
+        best = fmaxf(best, top);
+        if (--left == 0 || !more) note();
       }
       if (more) {
 #pragma unroll
@@ -246,57 +339,200 @@ __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
       const float d = (end - run.m) * c, x = __builtin_amdgcn_exp2f(d);
       run.s += x;
       run.a += x * fmaxf(d, kFar);
-      if constexpr (TOP) list.offer(end_off != ~0u ? key_of(end, index0 + end_off) : 0, a.top);
     }
     run.wave_join(c);
     if (lane == 0) {
       const u32x4 rec = {__float_as_uint(run.m), __float_as_uint(run.s), __float_as_uint(run.a), __float_as_uint(z)};
       reinterpret_cast<u32x4*>(as_global(a.part))[item] = rec;
+      if constexpr (TOP) {
+        // where the piece lies: address of its units (and, above it, the
+        // elements before and after them), their number, first index
+        const uint64_t where = (uint64_t)(uintptr_t)units | (uint64_t)pc.head << 56 | (uint64_t)pc.tail << 60;
+        const u32x4 place = {(uint32_t)where, (uint32_t)(where >> 32), pc.units, index0 + pc.head};
+        reinterpret_cast<u32x4*>(as_global(a.places))[item] = place;
+      }
     }
-    if constexpr (TOP)
-      if ((int)lane < a.top) as_global(a.keys)[item * (uint64_t)a.top + lane] = list.key;
+    if constexpr (TOP) {
+      while (seg < a.plan.segs) note();
+    }
   }
-}
-
-// The largest of the lanes' keys, on every lane: by the upper words, and by
-// the lower ones only where these tie.
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-  for (int off = 1; off < kWave; off <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off));
-  return v;
-}
-__device__ __forceinline__ unsigned long long wave_max_key(unsigned long long k) {
-  const uint32_t hi = (uint32_t)(k >> 32), top = wave_max_u32(hi);
-  const unsigned long long tie = __ballot(hi == top);
-  if ((tie & (tie - 1)) == 0) return TopList::lane_value(k, __builtin_ctzll(tie));
-  return ((unsigned long long)top << 32) | wave_max_u32(hi == top ? (uint32_t)k : 0u);
 }
 
 // What the join needs beside its output pointers.
 struct JoinInput {
   const float* part;
-  const unsigned long long* keys;
+  const uint32_t* places;
+  const float* bests;
   const int64_t* targets;
-  uint64_t rows;
+  uint64_t rows, first_row;
   int64_t vocab;
   float scale;
-  int p, top, pieces;
+  int p, top, pieces, segs, seg_steps;
 };
 
+// The largest elements of a row's groups, kLoads to a lane, in one go.
+constexpr int kLoads = kMaxGroups / kWave;
+__device__ __forceinline__ void load_bests(const JoinInput& a, uint64_t row, int lane, float (&v)[kLoads]) {
+  const int n = a.pieces * a.segs * kSegGroups;
+  const float* bests = as_global(a.bests) + row * (uint64_t)n;
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) v[i] = i * kWave + lane < n ? bests[i * kWave + lane] : -__builtin_inff();
+}
+
+// A piece as its wave wrote it down: the address of its units, the elements
+// before and after them, their number, the vocabulary index of their first.
+struct Place {
+  const uint8_t* units;
+  uint32_t head, tail, n, index;
+  __device__ __forceinline__ Place(u32x4 v)
+      : units(as_global((const uint8_t*)(uintptr_t)((((uint64_t)v[1] << 32) | v[0]) & 0xffffffffffffffull))),
+        head(v[1] >> 24 & 15), tail(v[1] >> 28), n(v[2]), index(v[3]) {}
+};
+__device__ __forceinline__ u32x4 lane_place(u32x4 place, int lane) {
+  u32x4 v;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) v[d] = (uint32_t)__shfl((int)place[d], lane);
+  return v;
+}
+
+// The k best elements of a row, one per lane in descending order (0: fewer).
+// place: this lane's piece; v: load_bests.  One wave runs through this code
+// once, so it is short rather than unrolled.
+template <int DT>
+__device__ __forceinline__ unsigned long long row_best(const JoinInput& a, u32x4 place, const float (&v)[kLoads], int lane,
+                                                       JoinStore& st) {
+  using S = typename Traits<DT>::S;
+  constexpr int E = kElems<DT>;
+  const float bar = bar_of(largest(v), a.top);
+  // the groups whose elements reach the bar
+  Bag<uint32_t, kBagMost> groups{st.groups};
+  uint32_t hits = 0;
+#pragma unroll
+  for (int i = kLoads - 1; i >= 0; --i) hits = hits + hits + (v[i] >= bar);  // bit i
+  for (; __any(hits); hits &= hits - 1) groups.push((uint32_t)__builtin_ctz(hits | 1u << 31) * kWave + lane, hits);
+  wave_fence();
+  // Their units, a power of two of lanes to a group, four units to a lane.
+  constexpr int kBatch = 4, kWords = 4 * kBatch;
+  Bag<unsigned long long, kBagMost> keys{st.keys};
+  const uint32_t units_of = (uint32_t)a.seg_steps * (kStep / E) * kGroupLanes, wide = min(units_of, (uint32_t)kWave), per = kWave / wide;
+  const uint32_t count = groups.full() ? 0 : groups.n;
+  for (uint32_t g0 = 0; g0 < count; g0 += kBatch * per)
+    for (uint32_t m1 = 0; m1 < units_of && !keys.full(); m1 += wide) {
+      uint32_t word[kWords], index[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const uint32_t g = g0 + k * per + lane / wide, id = g < count ? st.groups[g] : 0;
+        const uint32_t m = m1 + lane % wide, seg = id / kSegGroups, piece = seg / (uint32_t)a.segs;
+        const uint32_t round = (seg - piece * a.segs) * (uint32_t)a.seg_steps * (kStep / E) + m / kGroupLanes;
+        const uint32_t u = round * kWave + id % kSegGroups * kGroupLanes + m % kGroupLanes;
+        const Place pl(lane_place(place, (int)piece));
+        const RawUnit<DT, E> raw = g < count && m < units_of && u < pl.n ? load_unit<DT, E, false>(pl.units, (uint64_t)u * E) : masked_unit<DT>();
+#pragma unroll
+        for (int d = 0; d < 4; ++d) word[4 * k + d] = raw.v[0][d];
+        index[k] = pl.index + u * E;
+      }
+      hits = 0;  // bit b: element b of the lane's
+#pragma unroll
+      for (int w = kWords - 1; w >= 0; --w) {
+        if constexpr (DT == kBF16) {
+          hits = hits + hits + (__uint_as_float(word[w] & 0xffff0000u) >= bar);
+          hits = hits + hits + (__uint_as_float(word[w] << 16) >= bar);
+        } else {
+          hits = hits + hits + (__uint_as_float(word[w]) >= bar);
+        }
+      }
+      for (; __any(hits); hits &= hits - 1) {
+        const uint32_t b = (uint32_t)__builtin_ctz(hits | 1u << 31), w = b / (E / 4);
+        uint32_t x = word[0], first = index[0];
+#pragma unroll
+        for (int i = 1; i < kWords; ++i) x = w == (uint32_t)i ? word[i] : x;
+#pragma unroll
+        for (int k = 1; k < kBatch; ++k) first = b / E == (uint32_t)k ? index[k] : first;
+        if constexpr (DT == kBF16) x = b % 2 ? x & 0xffff0000u : x << 16;
+        keys.push(key_of(__uint_as_float(x), first + b % E), hits);
+      }
+    }
+  // the elements before and after the pieces' units
+  if (__any(place[1] >> 24)) {
+    for (int i = 0; i < a.pieces * 16; i += kWave) {
+      const uint32_t piece = (uint32_t)(i + lane) / 16, l = (uint32_t)lane % 16;
+      const Place pl(lane_place(place, (int)(piece % kWave)));
+      const bool before = l < pl.head, after = l >= 8 && l - 8 < pl.tail;
+      const int64_t off = before ? (int64_t)l - pl.head : (int64_t)pl.n * E + l - 8;
+      float f = -__builtin_inff();
+      if ((before || after) && piece < (uint32_t)a.pieces) f = widen1<DT>(reinterpret_cast<const S*>(pl.units)[off]);
+      keys.push(key_of(f, pl.index + (uint32_t)off), f >= bar);
+    }
+  }
+  unsigned long long mine = 0;
+  if (!groups.full() && !keys.full()) {
+    const uint32_t n = keys.n;
+    if (lane < a.top) st.sorted[lane] = 0;
+    wave_fence();
+    for (uint32_t i = lane; i < n; i += kWave) {
+      const unsigned long long k = st.keys[i];
+      uint32_t rank = 0;
+#pragma unroll 8
+      for (uint32_t j = 0; j < n; ++j) rank += st.keys[j] > k;
+      if (rank < (uint32_t)a.top) st.sorted[rank] = k;
+    }
+    wave_fence();
+    if (lane < a.top) mine = st.sorted[lane];
+    wave_fence();
+  } else {
+    // more ties with the bar, or more of the best in few lanes, than there
+    // is room for: the whole row again, by insertion
+    TopList list;
+    for (int i = 0; i < a.pieces; ++i) {
+      u32x4 at;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) at[d] = (uint32_t)__builtin_amdgcn_readlane((int)place[d], i);
+      const Place pl(at);
+      const bool before = (uint32_t)lane < pl.head, after = lane >= 8 && (uint32_t)lane - 8 < pl.tail;
+      const int64_t off = before ? (int64_t)lane - pl.head : (int64_t)pl.n * E + lane - 8;
+      list.offer(before || after ? key_of(widen1<DT>(reinterpret_cast<const S*>(pl.units)[off]), pl.index + (uint32_t)off) : 0, a.top);
+      for (uint32_t u0 = 0; u0 < pl.n; u0 += kBatch * kWave) {
+        RawUnit<DT, E> raw[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const uint32_t u = u0 + k * kWave + lane;
+          raw[k] = u < pl.n ? load_unit<DT, E, false>(pl.units, (uint64_t)u * E) : masked_unit<DT>();
+        }
+#pragma unroll 1
+        for (int k = 0; k < kBatch; ++k) {
+          float f[E];
+          widen_unit(raw[0], f);
+#pragma unroll
+          for (int j = 0; j + 1 < kBatch; ++j) raw[j] = raw[j + 1];
+          const float top = largest(f);
+          const uint32_t u = u0 + k * kWave + lane;
+          if (__any(order_of(top) >= (uint32_t)(list.bar >> 32))) list.consider(f, top, pl.index + u * E, u < pl.n, a.top);
+        }
+      }
+    }
+    mine = list.key;
+  }
+  return lane < a.top ? mine : 0;
+}
+
+template <int DT, bool TOP>
 __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinInput a, LogprobJoinArgs j) {
+  __shared__ JoinStore store[TOP ? kBlock / kWave : 1];
   const int lane = (int)(threadIdx.x % kWave), pieces = a.pieces;
   const float c = a.scale * kLog2e, inf = __builtin_inff(), nan = __uint_as_float(0x7fc00000u);
-  const uint64_t step = (uint64_t)gridDim.x * (kBlock / kWave);
-  uint64_t row = (uint64_t)blockIdx.x * (kBlock / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  for (; row < a.rows; row += step) {
+  const uint64_t row = a.first_row + (uint64_t)blockIdx.x * (kBlock / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (row < a.rows) {
     Running run;
-    float z = -inf;
+    float z = -inf, bests[kLoads];
+    if constexpr (TOP) load_bests(a, row, lane, bests);
+    u32x4 place = {0, 0, 0, 0};
     if (lane < pieces) {
       const u32x4 rec = reinterpret_cast<const u32x4*>(as_global(a.part))[row * (uint64_t)pieces + lane];
       run.m = __uint_as_float(rec[0]);
       run.s = __uint_as_float(rec[1]);
       run.a = __uint_as_float(rec[2]);
       z = __uint_as_float(rec[3]);
+      if constexpr (TOP) place = reinterpret_cast<const u32x4*>(as_global(a.places))[row * (uint64_t)pieces + lane];
     }
     z = wave_max(z);
     const int64_t target = as_global(a.targets)[row];
@@ -312,35 +548,33 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinInput a, Logpr
       as_global(j.logp[lane])[row] = !counts ? 0.0f : empty ? -inf : (z - m) * a.scale - log_s;
       if (j.entropy[lane]) as_global(j.entropy[lane])[row] = empty ? 0.0f : log_s - run.a * kLn2 / run.s;
     }
-    if (a.top == 0) continue;
-    // merge the pieces' descending lists: a lane holds its list's next two
-    const unsigned long long* list = as_global(a.keys) + (row * (uint64_t)pieces + lane) * a.top;
-    unsigned long long head = lane < pieces ? list[0] : 0, next = lane < pieces && a.top > 1 ? list[1] : 0, best = 0;
-    int at = 2;
-    for (int k = 0; k < a.top; ++k) {
-      const unsigned long long w = wave_max_key(head);
-      if (lane == k) best = w;
-      if (head == w && w) {
-        head = next;
-        next = at < a.top ? list[at] : 0;
-        ++at;
+    if constexpr (TOP) {
+      const unsigned long long best = poison || empty ? 0 : row_best<DT>(a, place, bests, lane, store[threadIdx.x / kWave]);
+      const int have = __popcll(__ballot(best != 0));
+      float lp = poison ? nan : best ? (value_of((uint32_t)(best >> 32)) - m) * a.scale - log_s : -inf;
+      int32_t idx = poison || !best ? -1 : (int32_t)~(uint32_t)best;
+      if (have < a.top && !poison) {
+        // fewer unmasked entries than asked for: then the masked ones, lowest
+        // index first (at most 31 of the first 64 are listed)
+        bool free = lane < a.vocab;
+        for (int k = 0; k < have; ++k) free = free && __builtin_amdgcn_readlane(idx, k) != lane;
+        unsigned long long left = __ballot(free);
+        for (int k = have; k < a.top && left; ++k, left &= left - 1)
+          if (lane == k) idx = __builtin_ctzll(left);
       }
+      if (lane < a.top)
+  #pragma unroll 4
+        for (int r = 0; r < a.p; ++r) {
+          as_global(j.top_logp[r])[row * (uint64_t)a.top + lane] = lp;
+          as_global(j.top_idx[r])[row * (uint64_t)a.top + lane] = idx;
+        }
     }
-    const bool have = best != 0 && !poison;
-    const float v = value_of((uint32_t)(best >> 32));
-    const float lp = poison ? nan : !have || empty ? -inf : (v - m) * a.scale - log_s;
-    const int32_t idx = have ? (int32_t)~(uint32_t)best : -1;
-    if (lane < a.top)
-      for (int r = 0; r < a.p; ++r) {
-        as_global(j.top_logp[r])[row * (uint64_t)a.top + lane] = lp;
-        as_global(j.top_idx[r])[row * (uint64_t)a.top + lane] = idx;
-      }
   }
 }
 
 // Gradient.  A wave takes kGradLen elements of one row's shard, cut as the
 // forward pass's pieces.
-constexpr int64_t kGradLen = kWaveStep;
+constexpr int64_t kGradLen = kLogprobStep;
 
 struct GradRow {
   float m, shift, gl, gh, h, scale, c;
@@ -447,7 +681,7 @@ int pieces_of(int64_t vocab, int64_t len) { return vocab ? (int)((vocab + 7 + le
 // over all rows, and none over 32768 elements, as far as a row's 64 pieces
 // allow.
 void logprob_plan(int p, uint64_t rows, const int64_t* vocab, LogprobPlan* plan) {
-  const int64_t unit = kWaveStep, most = kMaxPieces / p;
+  const int64_t unit = kLogprobStep, most = kMaxPieces / p;
   const uint64_t want = rows ? (8192 + rows * (uint64_t)p - 1) / (rows * (uint64_t)p) : 1;
   plan->first[0] = 0;
   for (int r = 0; r < p; ++r) {
@@ -459,11 +693,17 @@ void logprob_plan(int p, uint64_t rows, const int64_t* vocab, LogprobPlan* plan)
     plan->first[r + 1] = plan->first[r] + pieces_of(vocab[r], len);
   }
   plan->pieces = plan->first[p];
+  // as many groups as there may be, of whole steps
+  int64_t steps = 1;
+  for (int r = 0; r < p; ++r) steps = std::max(steps, (std::min(plan->len[r], vocab[r]) + unit - 1) / unit);
+  const int64_t segs = std::min<int64_t>(steps, kMaxGroups / kSegGroups / std::max(plan->pieces, 1));
+  plan->seg_steps = (int)((steps + segs - 1) / segs);
+  plan->segs = (int)((steps + plan->seg_steps - 1) / plan->seg_steps);
 }
 
 int launch_logprob(int dtype, const LogprobArgs& a, const LogprobJoinArgs& j, void* stream) {
   hipStream_t s = (hipStream_t)stream;
-  const dim3 grid(wave_grid(a.rows * (uint64_t)a.plan.pieces)), join(wave_grid(a.rows)), block(kBlock);
+  const dim3 grid(wave_grid(a.rows * (uint64_t)a.plan.pieces)), block(kBlock);
   if (dtype == kF32) {
     if (a.top) hipLaunchKernelGGL((logprob_pieces_kernel<kF32, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((logprob_pieces_kernel<kF32, false>), grid, block, 0, s, a);
@@ -473,8 +713,16 @@ int launch_logprob(int dtype, const LogprobArgs& a, const LogprobJoinArgs& j, vo
   }
   const int e = (int)hipGetLastError();
   if (e) return e;
-  const JoinInput in{a.part, a.keys, a.targets, a.rows, a.first_index[a.p], a.scale, a.p, a.top, a.plan.pieces};
-  hipLaunchKernelGGL(logprob_join_kernel, join, block, 0, s, in, j);
+  JoinInput in{a.part, a.places, a.bests, a.targets, a.rows, 0, a.first_index[a.p], a.scale, a.p, a.top, a.plan.pieces,
+               a.plan.segs, a.plan.seg_steps};
+  // one row to a wave, so that nothing is hoisted out of a loop of one turn
+  constexpr uint64_t kMost = (uint64_t)0x1000000 * (kBlock / kWave);
+  for (; in.first_row < a.rows; in.first_row += kMost) {
+    const dim3 join(wave_grid(a.rows - in.first_row));
+    if (!a.top) hipLaunchKernelGGL((logprob_join_kernel<kF32, false>), join, block, 0, s, in, j);
+    else if (dtype == kF32) hipLaunchKernelGGL((logprob_join_kernel<kF32, true>), join, block, 0, s, in, j);
+    else hipLaunchKernelGGL((logprob_join_kernel<kBF16, true>), join, block, 0, s, in, j);
+  }
   return (int)hipGetLastError();
 }
 

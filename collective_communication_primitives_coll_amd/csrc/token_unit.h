@@ -291,7 +291,7 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint64_t hidden, uint6
 }
 
 // ---------------------------------------------------------------------------
-// Sums and maxima over a wave (or its runs of 16 lanes), on every lane, in
+// Sums and maxima over a wave (or its runs of 8 or 16 lanes), on every lane, in
 // one fixed order: 16 lanes by DPP, then across these with the gfx950 lane
 // swaps, so that no step goes through LDS.
 // ---------------------------------------------------------------------------
@@ -304,6 +304,7 @@ __device__ __forceinline__ float wave_fold(float v, F f) {
   v = f(v, dpp_move<0xB1>(v));   // quad_perm 1,0,3,2
   v = f(v, dpp_move<0x4E>(v));   // quad_perm 2,3,0,1
   v = f(v, dpp_move<0x141>(v));  // row_half_mirror
+  if constexpr (LANES == 8) return v;
   v = f(v, dpp_move<0x140>(v));  // row_mirror
   if constexpr (LANES == 16) return v;
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -315,8 +316,9 @@ template <int LANES = kWave>
 __device__ __forceinline__ float wave_sum(float v) {
   return wave_fold<LANES>(v, [](float a, float b) { return a + b; });
 }
+template <int LANES = kWave>
 __device__ __forceinline__ float wave_max(float v) {
-  return wave_fold(v, [](float a, float b) { return fmaxf(a, b); });
+  return wave_fold<LANES>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 }  // namespace coll
