@@ -228,6 +228,7 @@ constexpr int kLogprobStep = 2048;
 constexpr int kMaxGroups = 1024, kGroupLanes = 8, kSegGroups = 64 / kGroupLanes;
 struct LogprobPlan {
   int pieces;                    // per row, over all ranks
+  uint64_t ranks_q32;            // ranks to a piece on average, times 2^32: where a piece's rank is first sought
   int segs, seg_steps;           // a piece's segments, of kSegGroups groups each, and the steps of one
   int first[kMaxRanks + 1];      // first piece of each rank, and the end
   int64_t len[kMaxRanks];        // elements per piece (the rank's last may be shorter)
@@ -241,7 +242,7 @@ struct LogprobArgs {
   float* part;                   // [rows][pieces][4]: max, sum, entropy sum, target's logit (-inf where elsewhere)
   uint32_t* places;              // with alternatives: [rows][pieces][4], where each piece lies
   float* bests;                  // with alternatives: [rows][pieces][segs][kSegGroups], largest elements
-  uint64_t rows;
+  uint64_t rows, first_row;      // this launch's
   float scale;                   // inverse temperature
   int p;
   int top;
@@ -264,7 +265,7 @@ struct LogprobGradArgs {
   const float* dlogp;
   const float* entropy;          // null without dentropy
   const float* dentropy;
-  uint64_t rows;
+  uint64_t rows, first_row;      // this launch's
   float scale;
   int p;
 };
