@@ -31,16 +31,18 @@
 // in each piece, whose end no other work hides, 127 us; groups of one lane's
 // elements over a whole piece, each in a line of its own, 110 us.)
 //
-// Sums run in base 2 (v_exp_f32), in fp32.  Differences to the maximum are
-// taken before the scaling, so large logits lose nothing, and are held at
-// -16384 or more where they multiply a sum, so that no 0 * inf arises.  The
+// Sums run in base 2 (v_exp_f32), in fp32.  A difference to the maximum is
+// one fma, whose known rounding is taken back out of the sums; where the
+// maximum or the scale is large, or an entry masked, it is taken before the
+// scaling, so that large logits lose nothing, and held at -16384 or more
+// where it multiplies a sum, so that no 0 * inf arises.  The
 // running maximum starts at the lowest finite value: a masked entry
 // (-infinity) then always contributes zero, and a row with nothing else
 // has S = 0.  A NaN or +infinity makes S a NaN.
 //
-// Gradient: 4 bytes an element in bf16, read once and written once.  2048 x
-// 131072 bf16 in 8 column slices of one matrix: 171 us, 6.28 TB/s, what a
-// stream read and written one to one reaches on this card.
+// Gradient: 4 bytes an element in bf16, read once and written once.  4096 x
+// 65536 bf16 in 8 shards: 171 us, 6.28 TB/s, what a stream read and written
+// one to one reaches on this card.
 #include <float.h>
 
 #include <algorithm>
