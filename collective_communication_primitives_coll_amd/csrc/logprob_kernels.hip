@@ -132,8 +132,10 @@ struct TopList {
 };
 
 // A piece of a row's shard: its elements before the first 16-byte boundary,
-// its whole units and the rest.  Pieces after the first start on such a
-// boundary, so only a shard's two ends go element by element.
+// its whole units and the rest.  Pieces after the first start on a 128-byte
+// line, so that no two waves share one and only a shard's two ends go element
+// by element.
+constexpr int kLine = 128;
 struct Piece {
   int64_t begin;       // first element
   uint32_t head, tail; // elements
@@ -142,7 +144,7 @@ struct Piece {
 template <int DT>
 __device__ __forceinline__ Piece piece_of(const uint8_t* row, int64_t vocab, int64_t len, int k) {
   constexpr int B = Traits<DT>::B, E = kElems<DT>;
-  const int64_t mis = (int64_t)((uintptr_t)row & 15) / B;
+  const int64_t mis = (int64_t)((uintptr_t)row % kLine) / B;
   Piece c;
   c.begin = k ? (int64_t)k * len - mis : 0;
   int64_t end = (int64_t)(k + 1) * len - mis;
@@ -603,12 +605,12 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinInput a, Logpr
   }
 }
 
-// Gradient.  A wave takes UNITS * 64 16-byte units of one row's shard, cut as
-// the forward pass's pieces:
-// 2048 elements (4 or 8 units to a lane), or 1024 of bf16 where all rows are
-// 16-byte aligned: 4096 x 32000 then takes 89 us instead of 95, 2048 x 131072
-// 178 instead of 179; unaligned rows, whose pieces share 128-byte lines, lose
-// by it (256 x 50257: 12.5 instead of 11.5).
+// Gradient.  A wave takes two 16-byte units a lane of one row's shard, 2 KiB
+// cut as the forward pass's pieces.  The card then works in a narrow window of
+// memory: four units of bf16 took 181 us instead of 171 for 4096 x 65536, and
+// four and eight of fp32 179 and 181 instead of 173 for 4096 x 32000.
+constexpr int kGradUnits = 2;
+
 // A row's gradient.  With d = log2 p_j, dz = 2^d (A + B d), but for the
 // target's own term.
 struct GradRow {
@@ -638,7 +640,7 @@ struct GradRow {
   }
 };
 
-template <int DT, int UNITS>
+template <int DT>
 __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(LogprobGradArgs a, LogprobPlan plan) {
   constexpr int B = Traits<DT>::B, E = kElems<DT>;
   using S = typename Traits<DT>::S;
@@ -650,12 +652,12 @@ __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(LogprobGradArgs a,
   const int64_t vocab = a.first_index[r + 1] - a.first_index[r];
   const uint8_t* base = as_global(static_cast<const uint8_t*>(a.logits[r])) + (int64_t)row * a.ld[r] * B;
   uint8_t* out = as_global(static_cast<uint8_t*>(a.dlogits[r])) + (int64_t)row * a.dld[r] * B;
-  const Piece pc = piece_of<DT>(base, vocab, UNITS * kWave * E, it.piece - plan.first[r]);
+  const Piece pc = piece_of<DT>(base, vocab, kGradUnits * kWave * E, it.piece - plan.first[r]);
   const RowBuffer units(base + (pc.begin + pc.head) * B, pc.units * 16);
   const RowBuffer outs(out + (pc.begin + pc.head) * B, pc.units * 16);
-  RawUnit<DT, E> x[UNITS];
+  RawUnit<DT, E> x[kGradUnits];
 #pragma unroll
-  for (int i = 0; i < UNITS; ++i) x[i] = load_unit<DT, E, true>(units, (i * kWave + lane) * E);
+  for (int i = 0; i < kGradUnits; ++i) x[i] = load_unit<DT, E, true>(units, (i * kWave + lane) * E);
 
   const int64_t target = ld_const(a.targets + row);
   const bool counts = target >= 0 && target < a.first_index[a.p];
@@ -687,7 +689,7 @@ __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(LogprobGradArgs a,
   };
   if (near) {
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
+    for (int i = 0; i < kGradUnits; ++i) {
       float f[E];
       widen_unit(x[i], f);
 #pragma unroll
@@ -696,7 +698,7 @@ __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(LogprobGradArgs a,
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < UNITS; ++i) {
+    for (int i = 0; i < kGradUnits; ++i) {
       float f[E];
       widen_unit(x[i], f);
 #pragma unroll
@@ -738,9 +740,9 @@ void finish_plan(LogprobPlan* plan, int p) {
   plan->ranks_q32 = ((uint64_t)p << 32) / (uint64_t)std::max(plan->pieces, 1);
 }
 
-// Pieces of `len` elements that cover a shard whatever its rows' offset from
-// a 16-byte boundary (at most 7 elements).
-int pieces_of(int64_t vocab, int64_t len) { return vocab ? (int)((vocab + 7 + len - 1) / len) : 0; }
+// Pieces of `len` elements that cover a shard whose rows start at most
+// `before` elements after a line's start.
+int pieces_of(int64_t vocab, int64_t before, int64_t len) { return vocab ? (int)((vocab + before + len - 1) / len) : 0; }
 
 }  // namespace
 
@@ -748,16 +750,16 @@ int pieces_of(int64_t vocab, int64_t len) { return vocab ? (int)((vocab + 7 + le
 // over all rows, and none over 32768 elements, as far as a row's 64 pieces
 // allow.
 void logprob_plan(int p, uint64_t rows, const int64_t* vocab, LogprobPlan* plan) {
-  const int64_t unit = kLogprobStep, most = kMaxPieces / p;
+  const int64_t unit = kLogprobStep, most = kMaxPieces / p, most_before = kLine / 2 - 1;
     const uint64_t want = rows ? (8192 + rows * (uint64_t)p - 1) / (rows * (uint64_t)p) : 1;
   plan->first[0] = 0;
   for (int r = 0; r < p; ++r) {
-    const int64_t v = vocab[r] + 7;
+    const int64_t v = vocab[r] + most_before;
     int64_t s = std::min<int64_t>(most, std::max<int64_t>((int64_t)std::min<uint64_t>(want, 64), (v + 32767) / 32768));
     s = std::max<int64_t>(1, std::min<int64_t>(s, (v + unit - 1) / unit));
     const int64_t len = ((v + s - 1) / s + 511) / 512 * 512;
     plan->len[r] = len;
-    plan->first[r + 1] = plan->first[r] + pieces_of(vocab[r], len);
+    plan->first[r + 1] = plan->first[r] + pieces_of(vocab[r], most_before, len);
   }
   finish_plan(plan, p);
   // as many groups as there may be, of whole steps
@@ -798,20 +800,18 @@ int launch_logprob(int dtype, const LogprobArgs& args, const LogprobJoinArgs& j,
 int launch_logprob_backward(int dtype, const LogprobGradArgs& args, void* stream) {
   hipStream_t s = (hipStream_t)stream;
   LogprobGradArgs a = args;
-  bool aligned = dtype == kBF16;
-  for (int r = 0; r < a.p; ++r)
-    aligned = aligned && !(((uintptr_t)a.logits[r] | (uintptr_t)a.dlogits[r] | (uint64_t)(a.ld[r] | a.dld[r]) * 2) & 15);
-  const int len = aligned ? kLogprobStep / 2 : kLogprobStep;
+  const int64_t B = dtype == kF32 ? 4 : 2, len = kGradUnits * kWave * 16 / B;
   LogprobPlan plan{};
-  for (int r = 0; r < a.p; ++r)
-    plan.first[r + 1] = plan.first[r] + pieces_of(a.first_index[r + 1] - a.first_index[r], len);
+  for (int r = 0; r < a.p; ++r) {
+    const int64_t before = a.ld[r] * B % kLine ? kLine / B - 1 : (int64_t)((uintptr_t)a.logits[r] % kLine) / B;
+    plan.first[r + 1] = plan.first[r] + pieces_of(a.first_index[r + 1] - a.first_index[r], before, len);
+  }
   finish_plan(&plan, a.p);
   return over_rows(args.rows, (uint64_t)plan.pieces, [&](uint64_t first, uint64_t rows, dim3 grid) {
     a.first_row = first;
     a.rows = rows;
-    if (dtype == kF32) hipLaunchKernelGGL((logprob_grad_kernel<kF32, 8>), grid, dim3(kBlock), 0, s, a, plan);
-    else if (aligned) hipLaunchKernelGGL((logprob_grad_kernel<kBF16, 2>), grid, dim3(kBlock), 0, s, a, plan);
-    else hipLaunchKernelGGL((logprob_grad_kernel<kBF16, 4>), grid, dim3(kBlock), 0, s, a, plan);
+    if (dtype == kF32) hipLaunchKernelGGL((logprob_grad_kernel<kF32>), grid, dim3(kBlock), 0, s, a, plan);
+    else hipLaunchKernelGGL((logprob_grad_kernel<kBF16>), grid, dim3(kBlock), 0, s, a, plan);
   });
 }
 
