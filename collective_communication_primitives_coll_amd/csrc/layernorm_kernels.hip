@@ -157,10 +157,33 @@ __device__ __forceinline__ uint64_t own_row(uint64_t block) {
 // three rows 155, four 159.  Persistent workgroups, with the weights in
 // registers and the next row's loads ahead, 166-175 us; rows claimed from
 // counters 158-164 us.
-// With the checkpoint, 8 x 2048 x 7168 bf16 and fp32 weights: 113 us
-// (5.3 TB/s), bound by how many rows the registers hold.
+// With the checkpoint, 8 x 2048 x 7168 bf16 and fp32 weights: 109 us
+// (5.4 TB/s), bound by how many rows the registers hold.  The codes are
+// stored in the first pass: 116-119 us after it, 115 us with the results.
 // ---------------------------------------------------------------------------
 constexpr int kRows = 2;
+
+// Whether the registers keep a bf16 row as it was loaded, to be widened again
+// in every pass, or its fp32 values, which take twice the room: where one
+// more workgroup then fits a CU.  16384 rows in 8 shards, us as loaded and
+// widened: 7168 with fp32 weights and checkpoints 109 and 117, 12288 plain
+// 134 and 156 (with fp32 weights 136 and 162); where no more fit, widening
+// costs: 7168 plain 77 and 76, 4096 with checkpoints 62 and 59, 12288 with
+// both 194 and 187, 16384 224 and 213.
+template <int DT, int WT, int TPR, bool CKPT>
+constexpr bool as_loaded() {
+  constexpr int more = (WT == kF32) + CKPT;
+  return DT == kBF16 && (TPR == 384 || TPR == 512 ? more >= 1 : TPR == 768 && more <= 1);
+}
+// The same unit, but not known to be.
+template <bool HIDE, int DT, int E>
+__device__ __forceinline__ RawUnit<DT, E>& again(RawUnit<DT, E>& r) {
+  if constexpr (HIDE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(r.v[0][i]));
+  }
+  return r;
+}
 
 template <int DT, int WT, int TPR, int NU, bool TAIL, bool CKPT>
 __global__ __launch_bounds__(block_of(TPR)) void ln_forward_kernel(LnArgs a) {
@@ -180,20 +203,26 @@ __global__ __launch_bounds__(block_of(TPR)) void ln_forward_kernel(LnArgs a) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) raw[k][i] = x.template get<true>(i * TPR + lane);
   }
-  float f[kRows][NU][E], s[kRows], q[kRows];
+  float s[kRows], q[kRows];
+  constexpr bool kHide = as_loaded<DT, WT, TPR, CKPT>();
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     s[k] = 0.0f;
+    uint8_t* ckpt = CKPT ? a.ckpt[rank] + (row0 + k) * a.row_bytes : nullptr;
+    const bool live = row0 + k < a.rows;
+    // (of a row to itself; where a wave holds several, by their addresses)
+    const RowBuffer codes(ckpt, live ? H : 0), scales(CKPT ? ckpt + H : nullptr, live ? (H >> a.glog) * 4 : 0);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const uint32_t u = i * TPR + lane, skip = TAIL && may_end<TPR, NU>(i) ? skip_of<E>(u, H) : 0;
-      widen_unit(raw[k][i], f[k][i]);
+      float f[E];
+      widen_unit(raw[k][i], f);
 #pragma unroll
-      for (uint32_t e = 0; e < E; ++e) s[k] += TAIL && may_end<TPR, NU>(i) && e < skip ? 0.0f : f[k][i][e];
+      for (uint32_t e = 0; e < E; ++e) s[k] += TAIL && may_end<TPR, NU>(i) && e < skip ? 0.0f : f[e];
       if constexpr (CKPT) {
-        const RawUnit<kE4M3, E> code = encode_unit<DT, E>(raw[k][i], f[k][i], a.glog);
-        if (E * u < H && row0 + k < a.rows)
-          store_codes<E, true>(a.ckpt[rank] + (row0 + k) * a.row_bytes, H, a.row_bytes, E * u, a.glog, code);
+        const RawUnit<kE4M3, E> code = encode_unit<DT, E>(raw[k][i], f, a.glog);
+        if constexpr (TPR >= kWave) store_codes<E, true>(codes, scales, E * u, a.glog, code);
+        else if (E * u < H && live) store_codes<E, true>(ckpt, H, a.row_bytes, E * u, a.glog, code);
       }
     }
   }
@@ -210,10 +239,11 @@ __global__ __launch_bounds__(block_of(TPR)) void ln_forward_kernel(LnArgs a) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const uint32_t u = i * TPR + lane, skip = TAIL && may_end<TPR, NU>(i) ? skip_of<E>(u, H) : 0;
-      float sq = 0.0f;
+      float sq = 0.0f, f[E];
+      widen_unit(again<kHide>(raw[k][i]), f);
 #pragma unroll
       for (uint32_t e = 0; e < E; ++e) {
-        const float d = f[k][i][e] - s[k];
+        const float d = f[e] - s[k];
         sq = TAIL && may_end<TPR, NU>(i) && e < skip ? sq : __builtin_fmaf(d, d, sq);
       }
       q[k] += !TAIL && E * u >= H ? 0.0f : sq;
@@ -227,13 +257,15 @@ __global__ __launch_bounds__(block_of(TPR)) void ln_forward_kernel(LnArgs a) {
     const Row<DT, E, TAIL> y(static_cast<uint8_t*>(a.y[rank]) + (row0 + k) * row_bytes, H);
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      float g[E], b[E];
+      float f[E], g[E], b[E];
+      widen_unit(again<kHide>(raw[k][i]), f);
       widen_unit(gamma[i], g);
       widen_unit(beta[i], b);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[k][i][e] = (f[k][i][e] - s[k]) * rstd * g[e] + b[e];
-      y.template put<true>(i * TPR + lane, narrow_unit<DT, E>(f[k][i]));
+      for (int e = 0; e < E; ++e) f[e] = (f[e] - s[k]) * rstd * g[e] + b[e];
+      y.template put<true>(i * TPR + lane, narrow_unit<DT, E>(f));
     }
+    if constexpr (CKPT && TPR >= kWave) pad_codes(a.ckpt[rank] + (row0 + k) * a.row_bytes, H, a.row_bytes, a.glog, lane);
     if (lane == 0) {
       if (a.mean[rank]) as_global(a.mean[rank])[row0 + k] = s[k];
       if (a.rstd[rank]) as_global(a.rstd[rank])[row0 + k] = rstd;

@@ -290,6 +290,26 @@ __device__ __forceinline__ void store_codes(uint8_t* row, uint64_t hidden, uint6
     for (uint64_t b = hidden + 4 * (hidden >> glog); b < row_bytes; b += 4) *reinterpret_cast<float*>(r + b) = 0.0f;
 }
 
+// The same without a branch, of a row's codes and scales in a buffer each;
+// pad_codes writes the zeros, once a row.
+template <int E, bool NT>
+__device__ __forceinline__ void store_codes(const RowBuffer& codes, const RowBuffer& scales, uint32_t at, uint32_t glog,
+                                            const RawUnit<kE4M3, E>& q) {
+  constexpr int CP = NT ? kCachePolicyNt : 0;
+  if constexpr (E == 4) {
+    __builtin_amdgcn_raw_buffer_store_b32(q.c[0], codes.rsrc, (int)at, 0, CP);
+  } else {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{q.c[0], q.c[1]}, codes.rsrc, (int)at, 0, CP);
+  }
+  const uint32_t off = (at & ((1u << glog) - 1)) == 0 ? (at >> glog) * 4 : 0x7ffffff0u;  // past any end: not stored
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(q.s), scales.rsrc, (int)off, 0, 0);
+}
+__device__ __forceinline__ void pad_codes(uint8_t* row, uint64_t hidden, uint64_t row_bytes, uint32_t glog, uint32_t lane) {
+  const uint64_t b = hidden + 4 * (hidden >> glog) + 4 * lane;
+  if (b < row_bytes) *reinterpret_cast<float*>(as_global(row) + b) = 0.0f;
+}
+
 // ---------------------------------------------------------------------------
 // Sums and maxima over a wave (or its runs of 8 or 16 lanes), on every lane, in
 // one fixed order: 16 lanes by DPP, then across these with the gfx950 lane
