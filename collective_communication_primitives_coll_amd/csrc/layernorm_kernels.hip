@@ -161,7 +161,11 @@ __device__ __forceinline__ uint64_t own_row(uint64_t block) {
 // (5.4 TB/s), bound by how many rows the registers hold.  The codes are
 // stored in the first pass: 116-119 us after it, 115 us with the results.
 // ---------------------------------------------------------------------------
-constexpr int kRows = 2;
+// Rows to a lane: one where two workgroups of 1024 lanes then fit a CU (bf16
+// without checkpoints: 8 x 2048 x 16384 179 us instead of 213; with them 255
+// and 249, in fp32 199 and 180, since their registers leave room for one).
+template <int DT, int TPR, bool CKPT>
+constexpr int rows_of() { return TPR == 1024 && DT == kBF16 && !CKPT ? 1 : 2; }
 
 // Whether the registers keep a bf16 row as it was loaded, to be widened again
 // in every pass, or its fp32 values, which take twice the room: where one
@@ -169,11 +173,11 @@ constexpr int kRows = 2;
 // widened: 7168 with fp32 weights and checkpoints 109 and 117, 12288 plain
 // 134 and 156 (with fp32 weights 136 and 162); where no more fit, widening
 // costs: 7168 plain 77 and 76, 4096 with checkpoints 62 and 59, 12288 with
-// both 194 and 187, 16384 224 and 213.
+// both 194 and 187.
 template <int DT, int WT, int TPR, bool CKPT>
 constexpr bool as_loaded() {
   constexpr int more = (WT == kF32) + CKPT;
-  return DT == kBF16 && (TPR == 384 || TPR == 512 ? more >= 1 : TPR == 768 && more <= 1);
+  return DT == kBF16 && (TPR == 384 || TPR == 512 ? more >= 1 : TPR == 768 ? more <= 1 : TPR == 1024 && !CKPT);
 }
 // The same unit, but not known to be.
 template <bool HIDE, int DT, int E>
@@ -188,6 +192,7 @@ __device__ __forceinline__ RawUnit<DT, E>& again(RawUnit<DT, E>& r) {
 template <int DT, int WT, int TPR, int NU, bool TAIL, bool CKPT>
 __global__ __launch_bounds__(block_of(TPR)) void ln_forward_kernel(LnArgs a) {
   constexpr int E = kElems<DT>;
+  constexpr int kRows = rows_of<DT, TPR, CKPT>();
   __shared__ float red[2][kRows][waves_of(TPR)];
   const int rank = blockIdx.y;
   const uint32_t lane = threadIdx.x % TPR, H = (uint32_t)a.hidden;
@@ -690,8 +695,8 @@ int forward_t(const LnArgs& a, bool ckpt, hipStream_t s) {
     return (int)hipGetLastError();
   }
   return with_shape(a.hidden, [&](auto T, auto N) {
-    constexpr int TPR = decltype(T)::value, NU = decltype(N)::value * 8 / kElems<DT>, RUN = block_of(TPR) / TPR * kRows;
-    const uint64_t runs = (a.rows + RUN - 1) / RUN;
+    constexpr int TPR = decltype(T)::value, NU = decltype(N)::value * 8 / kElems<DT>, RPB = block_of(TPR) / TPR;
+    const uint64_t run = RPB * (ckpt ? rows_of<DT, TPR, true>() : rows_of<DT, TPR, false>()), runs = (a.rows + run - 1) / run;
     if (runs > 0x7fffffffull) return (int)hipErrorInvalidConfiguration;
     const dim3 grid((uint32_t)runs, a.ranks), block(block_of(TPR));
     constexpr bool PACKED = TPR < kWave;  // several rows to a wave
