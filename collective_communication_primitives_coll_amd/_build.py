@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcoll.so")
 
 SOURCES = [
-    "coll_api.cpp",
+    "token_api.cpp",  # with coll_api.cpp
     "reduce_kernels.hip",
     "reduce_kernels_p3_7.hip",
     "reduce_kernels_p9_12.hip",

@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "token_args.h"
 
 namespace coll {
 
