@@ -31,7 +31,7 @@ namespace coll {
 
 namespace {
 
-constexpr int block_of(int tpr) { return tpr < kBlock ? kBlock : tpr; }
+constexpr int block_of(int tpr) { return tpr < kBlock && kBlock % tpr == 0 ? kBlock : tpr; }
 constexpr int waves_of(int tpr) { return tpr < kWave ? 1 : tpr / kWave; }
 
 // Sums over the TPR lanes of a row, R at once.  red: LDS.  One barrier: a
@@ -140,7 +140,7 @@ __device__ __forceinline__ void load_weights(const void* w, float absent, uint32
 // a time.
 template <int TPR>
 __device__ __forceinline__ uint64_t own_row(uint64_t block) {
-  if constexpr (TPR >= kBlock) return block;
+  if constexpr (block_of(TPR) == TPR) return block;
   if constexpr (TPR < kWave) return block * (kBlock / TPR) + threadIdx.x / TPR;
   return block * (kBlock / TPR) + __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
 }
@@ -657,10 +657,12 @@ __global__ __launch_bounds__(kJoinBlock) void ln_join_kernel(LnJoinArgs a) {
 // each) for a width, 0 lanes: the wide kernels' (or narrower than a unit).
 // At least half of the lanes' units lie in the row, except in the narrow
 // classes of 16 and 64 lanes.  (8 x 16384 rows of 128 bf16 took 15 us forward
-// and 37 us backward with 16 lanes to a row, 32 and 64 us with 64.)
+// and 37 us backward with 16 lanes to a row, 32 and 64 us with 64.  8 x 4096
+// rows of 2560: 80 and 91 us with checkpoints with 192 lanes, 88 and 94 with
+// 256.)
 void row_shape(uint64_t hidden, int* tpr, int* nu) {
   const uint64_t units = (hidden + 7) / 8;
-  *tpr = hidden < 8 ? 0 : units <= 32 ? 16 : units <= 128 ? 64 : units <= 512 ? 256 : units <= 768 ? 384 : units <= 1024 ? 512 : units <= 1536 ? 768 : units <= 2048 ? 1024 : 0;
+  *tpr = hidden < 8 ? 0 : units <= 32 ? 16 : units <= 128 ? 64 : units <= 256 ? 256 : units <= 384 ? 192 : units <= 512 ? 256 : units <= 768 ? 384 : units <= 1024 ? 512 : units <= 1536 ? 768 : units <= 2048 ? 1024 : 0;
   *nu = *tpr && units <= (uint64_t)*tpr ? 1 : 2;
 }
 
@@ -673,6 +675,7 @@ int with_shape(uint64_t hidden, F f) {
   const std::integral_constant<int, 2> two;
   if (tpr == 16) return nu == 1 ? f(std::integral_constant<int, 16>(), one) : f(std::integral_constant<int, 16>(), two);
   if (tpr == 64) return nu == 1 ? f(std::integral_constant<int, 64>(), one) : f(std::integral_constant<int, 64>(), two);
+  if (tpr == 192) return f(std::integral_constant<int, 192>(), two);
   if (tpr == 256) return nu == 1 ? f(std::integral_constant<int, 256>(), one) : f(std::integral_constant<int, 256>(), two);
   if (tpr == 384) return f(std::integral_constant<int, 384>(), two);
   if (tpr == 512) return f(std::integral_constant<int, 512>(), two);
@@ -739,12 +742,12 @@ int backward_t(const LnArgs& a, uint32_t groups, bool ckpt, hipStream_t s) {
 // and workspace must not depend on the device or on the grid limit).  One
 // workgroup of 512 lanes to a CU: 8 x 4096 x 7168 bf16 took 238 us with 256,
 // 252 with 512 and 279 with 384, whose second round is short.  Two of 256
-// lanes: 3 x 1777 x 2565 fp32 took 40 us with 512, 43.5 with 384, 45 and 48
-// with 768 and 1024, which write more partial sums.
+// lanes or less: 3 x 1777 x 2565 fp32 took 39 us with 512, 42 with 768, which
+// write more partial sums, and 43.5 with 384.
 uint32_t ln_backward_groups(int p, uint64_t rows, uint64_t hidden) {
   int tpr, nu;
   row_shape(hidden, &tpr, &nu);
-  const uint64_t rpb = tpr && tpr < kBlock ? kBlock / tpr : 1, all = rows * (uint64_t)std::min(p, kArgRanks), need = (all + rpb - 1) / rpb;
+  const uint64_t rpb = tpr ? block_of(tpr) / tpr : 1, all = rows * (uint64_t)std::min(p, kArgRanks), need = (all + rpb - 1) / rpb;
   const uint64_t most = tpr && tpr <= kBlock ? 512 : 256;
   return (uint32_t)std::max<uint64_t>(1, std::min(need, most));
 }

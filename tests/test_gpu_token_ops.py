@@ -114,6 +114,8 @@ LN_SHAPES = [
     (1, 1, 1), (2, 3, 7), (1, 5, 8), (3, 2, 9), (4, 6, 511), (1, 9, 512), (2, 4, 513), (2, 5, 1000), (1, 3, 1024), (1, 7, 1025),
     (3, 11, 2049), (2, 2, 4096), (1, 3, 4097), (8, 70, 7168), (1, 2, 8192), (1, 2, 8193), (2, 3, 16384), (1, 2, 16385), (2, 3, 20003),
     (33, 3, 72), (64, 2, 136), (1, 1500, 64), (5, 333, 100),
+    # the layouts whose lanes are no power of two
+    (2, 700, 2560), (1, 3, 3071), (3, 5, 4100), (2, 6, 5120), (1, 5, 6143), (1, 4, 8201), (2, 3, 10248), (1, 3, 12288),
 ]
 
 
@@ -371,7 +373,8 @@ def test_gated_activation_far_gates(coll):
 
 
 @pytest.mark.parametrize("dtype,wdtype", [(F32, F32), (BF16, BF16), (BF16, F32)])
-@pytest.mark.parametrize("p,rows,hidden,group", [(1, 1, 16, 16), (2, 9, 64, 32), (3, 5, 1536, 512), (8, 33, 7168, 128), (1, 3, 16384, 64), (2, 3, 20480, 512), (34, 2, 512, 16)])
+@pytest.mark.parametrize("p,rows,hidden,group", [(1, 1, 16, 16), (2, 9, 64, 32), (3, 5, 1536, 512), (8, 33, 7168, 128), (1, 3, 16384, 64), (2, 3, 20480, 512), (34, 2, 512, 16),
+                                                 (2, 700, 2560, 128), (1, 5, 5120, 64), (2, 3, 4608, 512), (1, 3, 12288, 16)])
 def test_layernorm_from_a_checkpoint(coll, p, rows, hidden, group, dtype, wdtype):
     import torch
     g = rng(14, p, rows, hidden, dtype, wdtype)
