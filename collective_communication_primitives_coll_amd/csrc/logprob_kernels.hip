@@ -26,7 +26,7 @@
 // whole 128-byte lines, and ranks the elements that reach it by counting.
 // 2048 rows of 131072 bf16: 88 us without alternatives, 102 us with 8, of
 // which the join takes 4 and 10: one wave's chain of loads, searches and
-// stores, as long for 4 rows (17 us in all) as for 2048.
+// stores, as long for 4 rows (15 us in all) as for 2048.
 // (Insertion into a sorted list while the chunks came took 120 us; a search
 // in each piece, whose end no other work hides, 127 us; groups of one lane's
 // elements over a whole piece, each in a line of its own, 110 us.)
@@ -207,11 +207,28 @@ __device__ __forceinline__ float largest(const float (&f)[N]) {
   return v;
 }
 
+// How many of a row's 16 values, each lane's row of 16, reach `mine`.
+template <int N = 0>
+__device__ __forceinline__ int reached_by(float y, float mine) {
+  const int one = dpp_move<N ? 0x120 + N : 0xE4>(y) >= mine;  // row_ror:N (0: as it is)
+  if constexpr (N < 15) return one + reached_by<N + 1>(y, mine);
+  return one;
+}
 // A bound that at least `top` lanes reach (or that all unmasked elements do).
 __device__ __forceinline__ float bar_of(float mine, int top) {
+  // the wave's four rows of 16 lanes, each on all rows
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(mine), __float_as_uint(mine), false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(a[0], a[0], false, false);
+  const auto c = __builtin_amdgcn_permlane32_swap(a[1], a[1], false, false);
+  uint32_t y[4] = {b[0], b[1], c[0], c[1]};
   int reached = 0;
-#pragma unroll 8
-  for (int j = 0; j < kWave; ++j) reached += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j)) >= mine;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    reached += reached_by(__uint_as_float(y[0]), mine);
+    y[0] = y[1];
+    y[1] = y[2];
+    y[2] = y[3];
+  }
   return fmaxf(wave_max(reached >= top ? mine : -FLT_MAX), -FLT_MAX);
 }
 
@@ -237,8 +254,8 @@ struct Bag {
 };
 constexpr uint32_t kBagMost = 256;
 struct JoinStore {
+  u32x4 groups[kBagMost];
   unsigned long long keys[kBagMost];
-  uint32_t groups[kBagMost];
   unsigned long long sorted[kMaxTop];
 };
 
@@ -426,43 +443,51 @@ __device__ __forceinline__ u32x4 lane_place(u32x4 place, int lane) {
 // place: this lane's piece; v: load_bests.  One wave runs through this code
 // once, so it is short rather than unrolled.
 template <int DT>
-__device__ __forceinline__ unsigned long long row_best(const JoinInput& a, u32x4 place, const float (&v)[kLoads], int lane,
+__device__ __forceinline__ unsigned long long row_best(const JoinInput& a, uint64_t row, u32x4 place, const float (&v)[kLoads], int lane,
                                                        JoinStore& st) {
   using S = typename Traits<DT>::S;
   constexpr int E = kElems<DT>;
   const float bar = bar_of(largest(v), a.top);
-  // the groups whose elements reach the bar
-  Bag<uint32_t, kBagMost> groups{st.groups};
+  // The groups whose elements reach the bar, as the address of their first
+  // unit, the units from there to the piece's end, the first's index.
+  Bag<u32x4, kBagMost> groups{st.groups};
   uint32_t hits = 0;
 #pragma unroll
   for (int i = kLoads - 1; i >= 0; --i) hits = hits + hits + (v[i] >= bar);  // bit i
   for (; __any(hits != 0); hits &= hits - 1) {
     const uint32_t id = (uint32_t)__builtin_ctz(hits | 1u << 31) * kWave + lane, seg = id / kSegGroups;
     const uint32_t piece = seg / (uint32_t)a.segs, round = (seg - piece * a.segs) * (uint32_t)a.seg_steps * (kStep / E);
-    // piece and first unit, which is a multiple of kGroupLanes
-    groups.push(piece | (round * kWave + id % kSegGroups * kGroupLanes) * (kMaxPieces / kGroupLanes), hits != 0);
+    const Place pl(lane_place(place, (int)(piece % kWave)));
+    const uint32_t u = round * kWave + id % kSegGroups * kGroupLanes;
+    const uint64_t at = (uint64_t)(uintptr_t)pl.units + (uint64_t)u * 16;
+    groups.push(u32x4{(uint32_t)at, (uint32_t)(at >> 32), pl.n - u, pl.index + u * E}, hits != 0);
   }
   wave_fence();
-  // Their units, a power of two of lanes to a group, eight units to a lane.
-  constexpr int kBatch = 8, kWords = 4 * kBatch;
+  // Their units, a power of two of lanes to a group, four units to a lane,
+  // loaded without a branch (what lies past an end from the row's own `part`, and masked).
+  constexpr int kBatch = 4, kWords = 4 * kBatch;
   Bag<unsigned long long, kBagMost> keys{st.keys};
   const uint32_t units_of = (uint32_t)a.seg_steps * (kStep / E) * kGroupLanes, wide = min(units_of, (uint32_t)kWave), per = kWave / wide;
   const uint32_t lane_g = wide == kWave ? 0 : lane / 32, lane_m = wide == kWave ? lane : lane % 32;
   const uint32_t count = groups.full() ? 0 : groups.n;
+  const uint64_t other = (uint64_t)(uintptr_t)a.part + row * (uint64_t)a.pieces * 16;
   for (uint32_t g0 = 0; g0 < count; g0 += kBatch * per)
     for (uint32_t m1 = 0; m1 < units_of && !keys.full(); m1 += wide) {
-      const uint32_t m = m1 + lane_m;
+      const uint32_t m = m1 + lane_m, u = m / kGroupLanes * kWave + m % kGroupLanes;
+      u32x4 group[kBatch], raw[kBatch];
       uint32_t word[kWords], index[kBatch];
+      bool in[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) group[k] = st.groups[min(g0 + k * per + lane_g, count - 1)];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const uint32_t g = g0 + k * per + lane_g, at = g < count ? st.groups[g] : 0;
-        const uint32_t u = at / kMaxPieces * kGroupLanes + m / kGroupLanes * kWave + m % kGroupLanes;
-        const Place pl(lane_place(place, (int)(at % kMaxPieces)));
-        const RawUnit<DT, E> raw = g < count && m < units_of && u < pl.n ? load_unit<DT, E, false>(pl.units, (uint64_t)u * E) : masked_unit<DT>();
-#pragma unroll
-        for (int d = 0; d < 4; ++d) word[4 * k + d] = raw.v[0][d];
-        index[k] = pl.index + u * E;
+        in[k] = g0 + k * per + lane_g < count && m < units_of && u < group[k][2];
+        index[k] = group[k][3] + u * E;
+        const uint64_t at = (((uint64_t)group[k][1] << 32) | group[k][0]) + (uint64_t)u * 16;
+        raw[k] = *as_global((const u32x4*)(uintptr_t)(in[k] ? at : other));
       }
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) word[w] = in[w / 4] ? raw[w / 4][w % 4] : masked_unit<DT>().v[0][w % 4];
       uint64_t hits = 0;  // bit b: element b of the lane's
 #pragma unroll
       for (int w = kWords - 1; w >= 0; --w) {
@@ -582,7 +607,7 @@ __global__ __launch_bounds__(kBlock) void logprob_join_kernel(JoinInput a, Logpr
       if (j.entropy[lane]) as_global(j.entropy[lane])[row] = empty ? 0.0f : log_s - run.a * kLn2 / run.s;
     }
     if constexpr (TOP) {
-      const unsigned long long best = poison || empty ? 0 : row_best<DT>(a, place, bests, lane, store[threadIdx.x / kWave]);
+      const unsigned long long best = poison || empty ? 0 : row_best<DT>(a, row, place, bests, lane, store[threadIdx.x / kWave]);
       const int have = __popcll(__ballot(best != 0));
       float lp = poison ? nan : best ? (value_of((uint32_t)(best >> 32)) - m) * a.scale - log_s : -inf;
       int32_t idx = poison || !best ? -1 : (int32_t)~(uint32_t)best;
