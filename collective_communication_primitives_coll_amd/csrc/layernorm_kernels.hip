@@ -20,8 +20,9 @@
 // Both the rows a workgroup takes and the number of workgroups depend on
 // the shape alone, so results never change from run to run.
 //
-// All sums are fp32 (a lane's partial sums run over at most a few hundred
-// rows before the join); bf16 results are narrowed once.
+// All sums are fp32 (a lane's partial sum runs over its workgroup's rows, one
+// in 256 or 512 of a large call's, before the join); bf16 results are
+// narrowed once.
 #include <algorithm>
 #include <type_traits>
 
@@ -662,7 +663,17 @@ __global__ __launch_bounds__(kJoinBlock) void ln_join_kernel(LnJoinArgs a) {
 // 256.)
 void row_shape(uint64_t hidden, int* tpr, int* nu) {
   const uint64_t units = (hidden + 7) / 8;
-  *tpr = hidden < 8 ? 0 : units <= 32 ? 16 : units <= 128 ? 64 : units <= 256 ? 256 : units <= 384 ? 192 : units <= 512 ? 256 : units <= 768 ? 384 : units <= 1024 ? 512 : units <= 1536 ? 768 : units <= 2048 ? 1024 : 0;
+  *tpr = hidden < 8      ? 0
+         : units <= 32   ? 16
+         : units <= 128  ? 64
+         : units <= 256  ? 256
+         : units <= 384  ? 192
+         : units <= 512  ? 256
+         : units <= 768  ? 384
+         : units <= 1024 ? 512
+         : units <= 1536 ? 768
+         : units <= 2048 ? 1024
+                         : 0;
   *nu = *tpr && units <= (uint64_t)*tpr ? 1 : 2;
 }
 

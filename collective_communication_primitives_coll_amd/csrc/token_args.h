@@ -57,8 +57,8 @@ struct Ckpt8Args {
   uint32_t glog;                 // log2 of a group's elements
 };
 
-// Vocabulary log probabilities over p shards.  A row's shard is cut into
-// segs[rank] pieces; all pieces of a row number at most kMaxPieces (a wave).
+// Vocabulary log probabilities over p shards.  A row's shards are cut into
+// pieces, at most kMaxPieces to a row (a wave's lanes).
 constexpr int kMaxPieces = 64;
 constexpr int kMaxTop = 32;
 // Elements that a wave takes in one step.
