@@ -878,7 +878,9 @@ def _targets(targets, rows: int | None):
     import torch
     if hasattr(targets, "dtype") and targets.dtype != torch.int64:
         raise ValueError("targets must be a device int64 tensor")
-    return _numel(targets, rows)
+    rows = _numel(targets, rows)
+    _check_sizes([targets], rows, "vocab_logprob targets")
+    return rows
 
 
 def coll_vocab_logprob_workspace_bytes(rows: int, vocab: Sequence[int], top_k: int = 0) -> int:

@@ -1,6 +1,7 @@
 """Host-side checks of the token-wise operators' entry points: refusals,
 workspaces, overlaps and empty calls, none of which reaches the device."""
 import ctypes
+import math
 
 import pytest
 
@@ -193,3 +194,50 @@ def test_binding_refuses_before_the_call():
         coll.coll_vocab_logprob_backward([1], 1, 1, 1, [1], rows=1, dtype=F32)              # raw addresses, no sizes
     with pytest.raises(ValueError):
         coll.coll_layernorm_backward([1], [1], [1], [1], None, [1], None, None, 1, 8, rows=1, dtype=F32)  # no workspace size
+
+
+class DeviceTensor:
+    """As much of a device tensor as the binding looks at, for deferred calls that are never made."""
+    is_cuda = True
+
+    def __init__(self, dtype, *shape, stride=None):
+        self.dtype, self.shape = dtype, shape
+        self.strides = stride or tuple(math.prod(shape[i + 1:]) for i in range(len(shape)))
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return math.prod(self.shape)
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def stride(self, i):
+        return self.strides[i]
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return BASE
+
+
+def _logprob_calls(n, targets=None, z=None, dz=None, **k):
+    """Deferred forward and backward calls of one rank's n rows of 100 entries."""
+    import torch
+    f = lambda *s: DeviceTensor(torch.float32, *s)  # noqa: E731
+    z, dz = z or f(n, 100), dz or f(n, 100)
+    t = DeviceTensor(torch.int64, n if targets is None else targets)
+    ws = DeviceTensor(torch.uint8, 1 << 20)
+    kf = {a: b for a, b in k.items() if a != "dld"}
+    return (lambda: coll.coll_vocab_logprob([z], t, [f(n, 2)], [f(n)], ws, defer=True, stream=0, **kf),
+            lambda: coll.coll_vocab_logprob_backward([z], t, f(n, 2), f(n), [dz], defer=True, stream=0, **k))
+
+
+def test_binding_refuses_targets_shorter_than_the_rows():
+    for call in _logprob_calls(5, 5) + _logprob_calls(5, 6, rows=5):
+        call()
+    for call in _logprob_calls(5, 4, rows=5):
+        with pytest.raises(ValueError, match="targets"):
+            call()
