@@ -722,10 +722,13 @@ def coll_layernorm_workspace_bytes(p: int, rows: int, hidden: int) -> int:
 
 
 def _workspace(ws, nbytes: int | None):
+    have = ws.numel() * ws.element_size() if hasattr(ws, "numel") else None
     if nbytes is None:
-        nbytes = ws.numel() * ws.element_size() if hasattr(ws, "numel") else None
+        nbytes = have
     if nbytes is None:
         raise ValueError("workspace_bytes must be given for raw addresses")
+    if have is not None and nbytes > have:
+        raise ValueError(f"workspace of {have} bytes, workspace_bytes is {nbytes}")
     return _addr(ws), int(nbytes)
 
 

@@ -241,3 +241,19 @@ def test_binding_refuses_targets_shorter_than_the_rows():
     for call in _logprob_calls(5, 4, rows=5):
         with pytest.raises(ValueError, match="targets"):
             call()
+
+
+def test_binding_refuses_workspace_bytes_past_the_tensor():
+    import torch
+    f = lambda *s: DeviceTensor(torch.float32, *s)  # noqa: E731
+    for call in _logprob_calls(5, workspace_bytes=1 << 20)[:1]:
+        call()
+    for call in _logprob_calls(5, workspace_bytes=(1 << 20) + 1)[:1]:
+        with pytest.raises(ValueError, match="workspace_bytes"):
+            call()
+    ws = DeviceTensor(torch.float32, 1000)
+    back = lambda n: coll.coll_layernorm_backward([f(5, 64)], [f(5, 64)], [f(5)], [f(5)], None, [f(5, 64)], None, None, ws, 64,  # noqa: E731
+                                                  workspace_bytes=n, defer=True, stream=0)
+    back(4000)
+    with pytest.raises(ValueError, match="workspace_bytes"):
+        back(4001)
