@@ -852,8 +852,8 @@ def _i64_array(vals):
 
 def _shard_array(xs, rows: int, vocab, ld, what: str):
     """Pointers, sizes and row strides of vocabulary shards: 2-d tensors
-    [rows, vocab] whose rows are contiguous (column slices included), or raw
-    addresses with vocab and ld given."""
+    [rows, vocab] whose rows are contiguous (column slices included; ld, if
+    given, is their stride), or raw addresses with vocab and ld given."""
     ptrs, vs, lds = [], [], []
     for i, x in enumerate(xs):
         if isinstance(x, int):
@@ -873,6 +873,8 @@ def _shard_array(xs, rows: int, vocab, ld, what: str):
         ptrs.append(x.data_ptr())
         vs.append(v)
         lds.append(max(int(x.stride(0)), v) if x.shape[0] <= 1 else int(x.stride(0)))
+        if ld is not None and x.shape[0] > 1 and int(ld[i]) != lds[-1]:
+            raise ValueError(f"{what}: rows {lds[-1]} elements apart, ld is {int(ld[i])}")
     arr, keep = _ptr_array(ptrs)
     return arr, _i64_array(vs), _i64_array(lds), keep
 

@@ -257,3 +257,16 @@ def test_binding_refuses_workspace_bytes_past_the_tensor():
     back(4000)
     with pytest.raises(ValueError, match="workspace_bytes"):
         back(4001)
+
+
+def test_binding_refuses_a_row_stride_that_is_not_the_tensors():
+    import torch
+    z = DeviceTensor(torch.float32, 5, 100, stride=(128, 1))
+    for call in _logprob_calls(5, z=z, ld=[128]) + _logprob_calls(5, z=z, dz=z, ld=[128], dld=[128])[1:]:
+        call()
+    one = DeviceTensor(torch.float32, 1, 100)
+    for call in _logprob_calls(1, z=one, ld=[999]):                                     # no second row
+        call()
+    for call in _logprob_calls(5, z=z, ld=[100]) + _logprob_calls(5, dz=z, dld=[100])[1:]:
+        with pytest.raises(ValueError, match="ld is 100"):
+            call()
