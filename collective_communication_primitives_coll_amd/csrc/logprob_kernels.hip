@@ -776,7 +776,8 @@ int pieces_of(int64_t vocab, int64_t before, int64_t len) { return vocab ? (int)
 // allow.
 void logprob_plan(int p, uint64_t rows, const int64_t* vocab, LogprobPlan* plan) {
   const int64_t unit = kLogprobStep, most = kMaxPieces / p, most_before = kLine / 2 - 1;
-    const uint64_t want = rows ? (8192 + rows * (uint64_t)p - 1) / (rows * (uint64_t)p) : 1;
+  // (rows past 8192 want one piece as 8192 do; their product with p may not fit)
+  const uint64_t shards = std::min<uint64_t>(rows, 8192) * (uint64_t)p, want = shards ? (8192 + shards - 1) / shards : 1;
   plan->first[0] = 0;
   for (int r = 0; r < p; ++r) {
     const int64_t v = vocab[r] + most_before;

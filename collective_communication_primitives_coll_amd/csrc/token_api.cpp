@@ -255,11 +255,12 @@ coll_status_t ln_backward(const void* const* dy, const void* const* x, bool from
 coll_status_t check_shards(const void* const* logits, const int64_t* ld, const int64_t* vocab, int p, size_t rows,
                            size_t d, int64_t (&first)[kMaxRanks + 1]) {
   if (!ld || !vocab) return COLL_ERR_INVALID_ARG;
+  size_t t;
+  if (!mul_ok(rows, 4 * coll::kMaxTop, 1, &t)) return COLL_ERR_INVALID_ARG;  // the widest of the arrays by row
   first[0] = 0;
   for (int r = 0; r < p; ++r) {
     if (vocab[r] < 0 || ld[r] < vocab[r] || vocab[r] > 0x7fffffffll) return COLL_ERR_INVALID_ARG;
     first[r + 1] = first[r] + vocab[r];
-    size_t t;
     if (!mul_ok((size_t)ld[r], rows, d, &t)) return COLL_ERR_INVALID_ARG;
   }
   if (first[p] < 1) return COLL_ERR_INVALID_ARG;

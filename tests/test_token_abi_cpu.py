@@ -2,10 +2,15 @@
 workspaces, overlaps and empty calls, none of which reaches the device."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
+import textwrap
 
 import pytest
 
 import collective_communication_primitives_coll_amd as coll
+from conftest import ROOT
 from test_abi_cpu import _arr, host_only
 
 OK, INV, UNS, AL = coll.COLL_OK, coll.COLL_ERR_INVALID_ARG, coll.COLL_ERR_UNSUPPORTED, coll.COLL_ERR_ALIAS
@@ -270,3 +275,34 @@ def test_binding_refuses_a_row_stride_that_is_not_the_tensors():
     for call in _logprob_calls(5, z=z, ld=[100]) + _logprob_calls(5, dz=z, dld=[100])[1:]:
         with pytest.raises(ValueError, match="ld is 100"):
             call()
+
+
+def test_logprob_of_rows_past_the_address_space():
+    """Row counts whose products leave 64 bits, in a process of its own: they must not end it."""
+    code = textwrap.dedent(f"""
+        import sys
+        sys.path.insert(0, {ROOT!r})
+        sys.path.insert(0, {os.path.join(ROOT, "tests")!r})
+        import collective_communication_primitives_coll_amd as coll
+        from test_token_abi_cpu import _i64
+        L = coll.lib()
+        for rows in (1 << 58, 1 << 60, (1 << 61) + 5, 1 << 62, 1 << 63, (1 << 64) - 1):
+            for p in (1, 3, 16, 64):
+                assert coll.coll_vocab_logprob_workspace_bytes(rows, [1] * p, 0) in (0, rows * p * 16), (rows, p)
+                assert coll.coll_vocab_logprob_workspace_bytes(rows, [1] * p, 4) == 0 or rows * p < 1 << 58
+                # (every pointer absent: no such call gets past the checks)
+                one = _i64(*[1] * p)
+                assert L.coll_vocab_logprob(None, one, one, None, 1.0, None, None, None, 0, None, None, p, rows, 1, None, 0, None) == 1
+                assert L.coll_vocab_logprob_backward(None, one, one, None, 1.0, None, None, None, None, None, one, p, rows, 1, None) == 1
+        print("through")
+    """)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "through" in r.stdout, (r.returncode, r.stderr[-2000:])
+
+
+@host_only
+def test_logprob_backward_refuses_rows_past_the_address_space():
+    L, b = coll.lib(), Bufs()
+    z, dz, t, st, dl, one = b(), b(), b.one(), b.one(), b.one(), _i64(1, 1, 1, 1)
+    for rows in (1 << 60, 1 << 61, 1 << 62):                            # 8 bytes a row leave 64 bits, or what an address may be
+        assert L.coll_vocab_logprob_backward(z, one, one, t, 1.0, st, dl, None, None, dz, one, P, rows, BF16, None) == INV
