@@ -440,15 +440,18 @@ __global__ __launch_bounds__(block_of(TPR)) void ln_backward_kernel(LnArgs a) {
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         const uint32_t skip = TAIL && may_end<TPR, NU>(i) ? skip_of<E>(i * TPR + lane, H) : 0;
+        // Past the row's end x and dy are zero, and so is all that dy enters,
+        // as long as n is finite there: without the mean, whose product with
+        // rstd may not be (a constant row of large values).
+        const float m = !TAIL && may_end<TPR, NU>(i) && E * (i * TPR + lane) >= H ? 0.0f : mean;
         float d[E], g[E];
         widen_unit(bx[k][i], n[i]);
         widen_unit(bd[k][i], d);
         widen_unit(gamma[i], g);
 #pragma unroll
         for (uint32_t e = 0; e < E; ++e) {
-          n[i][e] = (n[i][e] - mean) * rstd;
+          n[i][e] = (n[i][e] - m) * rstd;
           w[i][e] = d[e] * g[e];
-          // past the row's end dy is zero, and so is all that it enters
           const bool own = !(TAIL && may_end<TPR, NU>(i) && e < skip);
           const float de = own ? d[e] : 0.0f, we = own ? w[i][e] : 0.0f;
           dg[i][e] += own ? de * n[i][e] : 0.0f;
@@ -581,8 +584,9 @@ __global__ __launch_bounds__(1024) void ln_backward_wide_rows_kernel(LnArgs a) {
       widen_unit(row_unit<DT>(dy, u, full, part), w);
       weight_unit<WT>(a.gamma[rank], 1.0f, u, full, part, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        n[e] = (n[e] - mean) * rstd;
+      for (uint32_t e = 0; e < 8; ++e) {
+        // past the row's end zero, not -mean rstd, which may be infinite
+        n[e] = u < full || e < part ? (n[e] - mean) * rstd : 0.0f;
         w[e] *= g[e];
       }
     };

@@ -261,6 +261,42 @@ def test_layernorm_gradient_by_differences(coll):
             assert abs((loss(x, *a) - loss(x, *b)) / step - host(got[0])[j]) < lim
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("hidden", [7, 9, 136, 320, 1000, 1800, 2560, 3001, 4608, 7168, 9000, 12296, 20003])
+def test_layernorm_gradient_of_a_large_constant_row(coll, hidden, dtype):
+    """A constant row whose mean times 1 / sqrt(eps) passes fp32's range: its normalised values are 0 and its
+    gradient is finite, in every layout, whether the row fills its lanes or not."""
+    g = rng(21, hidden, dtype)
+    x = g.normal(0, 1, (3, hidden))
+    x[1] = 2.0 ** 110                                         # times 1e6: 1.3e39
+    x, xe = dev(x, dtype)
+    y, mean, rstd = new((3, hidden), dtype), f32(3), f32(3)
+    coll.coll_layernorm([x], None, None, [y], hidden, eps=1e-12, mean=[mean], rstd=[rstd])
+    assert (host(y)[1] == 0).all() and host(mean)[1] == 2.0 ** 110
+    m, s = host(mean), host(rstd)
+    assert m[1] * s[1] > 3.5e38
+    dy, dye = dev(g.normal(0, 1, (3, hidden)), dtype)
+    dx, dg, db = new((3, hidden), dtype), f32(hidden), f32(hidden)
+    ws = workspace(coll.coll_layernorm_workspace_bytes(1, 3, hidden))
+    dxe, dge, dbe, n = token_ops.layernorm_backward(dye, xe, m, s, np.ones(hidden))
+
+    def check(what):
+        close(host(dx), dxe, ln_backward_tol(dye, n, s, np.ones(hidden), dxe, dtype), f"dx {what}")
+        close(host(dg), dge, weight_tol(coll, 1, 3, hidden, np.abs(dye * n).sum(0), dge, F32), f"dgamma {what}")
+        close(host(db), dbe, weight_tol(coll, 1, 3, hidden, np.abs(dye).sum(0), dbe, F32), f"dbeta {what}")
+    coll.coll_layernorm_backward([dy], [x], [mean], [rstd], None, [dx], [dg], [db], ws, hidden, wdtype=F32)
+    check("of the rows")
+    if hidden % 64 == 0:
+        rows_e = token_ops.ckpt8_rows(xe.astype(np.float32), 32)
+        xe = token_ops.ckpt8_values(rows_e, hidden, 32).astype(np.float64)
+        assert (xe[1] == 2.0 ** 110).all()                    # 448 steps of its scale
+        ck = u8(3, coll.coll_ckpt8_row_bytes(hidden, 32))
+        coll.coll_ckpt8_save([x], [ck], hidden, 32)
+        dxe, dge, dbe, n = token_ops.layernorm_backward(dye, xe, m, s, np.ones(hidden))
+        coll.coll_layernorm_backward_ckpt8([dy], [ck], [mean], [rstd], None, [dx], [dg], [db], ws, hidden, 32, wdtype=F32)
+        check("of the checkpoint")
+
+
 # ----------------------------------------------------------------------------
 # 8-bit checkpoints
 # ----------------------------------------------------------------------------
