@@ -747,11 +747,11 @@ __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(LogprobGradArgs a,
 
 uint32_t wave_grid(uint64_t waves) { return (uint32_t)((waves + kBlock / kWave - 1) / (kBlock / kWave)); }
 
-// Calls f(first row, rows, blocks) for launches of at most 2^30 waves or one
-// row, `waves` to a row.
+// Calls f(first row, rows, blocks) for launches of as many rows as one may
+// have, `waves` waves to a row (2^22 at most, so that a row always fits).
 template <class F>
 int over_rows(uint64_t rows, uint64_t waves, F f) {
-  const uint64_t most = std::max<uint64_t>(1, ((uint64_t)1 << 30) / waves);
+  const uint64_t most = most_blocks(kBlock) * (kBlock / kWave) / waves;
   for (uint64_t first = 0; first < rows; first += most) {
     const uint64_t n = std::min(most, rows - first);
     f(first, n, dim3(wave_grid(n * waves)));

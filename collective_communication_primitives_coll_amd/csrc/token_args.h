@@ -11,6 +11,10 @@ namespace coll {
 // the 4 KiB of a kernel's arguments; more ranks take a second launch.
 constexpr int kArgRanks = 32;
 
+// Workgroups of a launch along a grid dimension, `block` work items each: HIP
+// takes fewer than 2^32 work items.
+constexpr uint64_t most_blocks(uint64_t block) { return 0xffffffffull / block; }
+
 struct LnArgs {
   const void* x[kArgRanks];      // rows; backward from a checkpoint: its rows
   const void* dy[kArgRanks];     // backward

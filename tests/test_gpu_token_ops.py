@@ -778,3 +778,39 @@ def test_rows_past_2_31_elements(coll):
     dxe, dge, _, n = token_ops.layernorm_backward(yb, xe, host(mean)[pick], host(rstd)[pick], np.ones(hidden))
     close(host(dx[pick]), dxe, ln_backward_tol(yb, n, host(rstd)[pick], np.ones(hidden), dxe, BF16), "dx")
     close(host(dg), dge, weight_tol(coll, 1, rows, hidden, np.abs(yb * n).sum(0), dge, F32), "dgamma")
+
+
+@pytest.mark.parametrize("p,rows", [(64, (1 << 20) + 3), (1, (1 << 26) + 5)])
+def test_logprob_of_more_rows_than_a_launch_holds(coll, p, rows):
+    """64 entries in 64 shards, and 2 in one: a launch ends 4 waves short of 2^26, so the last rows take another one,
+    the second time also in the join."""
+    import torch
+    v = max(p, 2)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(34)
+    z = torch.randn(rows, v, generator=gen, device="cuda").mul_(3).to(torch.bfloat16)
+    zs = [z[:, v * r // p:v * (r + 1) // p].contiguous() for r in range(p)]
+    tg = torch.randint(0, v, (rows,), generator=gen, device="cuda")
+    st, lp = f32(p, rows, 2), f32(p, rows)
+    ws = workspace(coll.coll_vocab_logprob_workspace_bytes(rows, [x.shape[1] for x in zs]))
+    coll.coll_vocab_logprob(zs, tg, list(st), list(lp), ws)
+    gl = torch.randn(rows, generator=gen, device="cuda")
+    dz = [torch.full_like(x, float("nan")) for x in zs]
+    coll.coll_vocab_logprob_backward(zs, tg, st[0], gl, dz)
+    torch.cuda.synchronize()
+    for a in range(0, rows, 1 << 24):
+        n = slice(a, min(rows, a + (1 << 24)))
+        d = z[n].double()
+        m = d.amax(1)
+        d -= m[:, None]
+        ls = d.exp().sum(1).log()
+        want = d.gather(1, tg[n, None])[:, 0] - ls
+        # differences of up to 40 and sums of up to 64: as check_logprob, no term above 300 U
+        for r in {0, p - 1}:
+            assert torch.equal(st[r][n, 0].double(), m)
+            assert float((st[r][n, 1].double() - ls).abs().max()) <= 300 * U
+            assert float((lp[r][n].double() - want).abs().max()) <= 300 * U
+        prob = (d - ls[:, None]).exp_()
+        ge = prob.neg_().scatter_add_(1, tg[n, None], torch.ones_like(want)[:, None]).mul_(gl[n, None].double())
+        got = torch.cat([x[n] for x in dz], 1).double()
+        assert bool(((got - ge).abs() <= HALF[BF16] * ge.abs() + 300 * U * gl[n, None].double().abs()).all())

@@ -1,6 +1,7 @@
 """Host-side checks of the token-wise operators' entry points: refusals,
 workspaces, overlaps and empty calls, none of which reaches the device."""
 import ctypes
+import json
 import math
 import os
 import subprocess
@@ -306,3 +307,97 @@ def test_logprob_backward_refuses_rows_past_the_address_space():
     z, dz, t, st, dl, one = b(), b(), b.one(), b.one(), b.one(), _i64(1, 1, 1, 1)
     for rows in (1 << 60, 1 << 61, 1 << 62):                            # 8 bytes a row leave 64 bits, or what an address may be
         assert L.coll_vocab_logprob_backward(z, one, one, t, 1.0, st, dl, None, None, dz, one, P, rows, BF16, None) == INV
+
+
+# ----------------------------------------------------------------------------
+# Launches of the largest shapes.  A stand-in for the runtime's launch calls
+# records them, so that the entry points run whole, on made-up addresses,
+# without a device.
+# ----------------------------------------------------------------------------
+
+RECORDER = r"""
+struct Dim { unsigned x, y, z; };
+static Dim grids[65536], blocks[65536], grid_now, block_now;
+static int n;
+extern "C" int __hipPushCallConfiguration(Dim grid, Dim block, unsigned long, void*) {
+  grid_now = grid, block_now = block;
+  return 0;
+}
+extern "C" int __hipPopCallConfiguration(Dim* grid, Dim* block, unsigned long* lds, void** stream) {
+  *grid = grid_now, *block = block_now, *lds = 0, *stream = nullptr;
+  return 0;
+}
+extern "C" int hipLaunchKernel(const void*, Dim grid, Dim block, void**, unsigned long, void*) {
+  if (n < 65536) { grids[n] = grid; blocks[n] = block; }
+  ++n;
+  return 0;
+}
+extern "C" int hipGetLastError() { return 0; }
+extern "C" int launches(unsigned* out) {
+  for (int i = 0; i < n && i < 65536; ++i, out += 6) {
+    out[0] = grids[i].x, out[1] = grids[i].y, out[2] = grids[i].z;
+    out[3] = blocks[i].x, out[4] = blocks[i].y, out[5] = blocks[i].z;
+  }
+  const int had = n;
+  n = 0;
+  return had;
+}
+"""
+
+
+class FarBufs(Bufs):
+    """Made-up rank arrays, a TiB apart."""
+
+    def __call__(self, p):
+        return super().__call__(p=p, step=1 << 40)
+
+    def one(self):
+        self.next += 1 << 40
+        return self.next - (1 << 40)
+
+
+def recorded(tmp_path, calls):
+    """The launches of each call, [(grid, block), ...] a call: `calls` are expressions of the C library L, the buffer
+    maker b and _i64, each giving a status."""
+    (tmp_path / "recorder.cpp").write_text(RECORDER)
+    so = tmp_path / "recorder.so"
+    subprocess.run(["g++", "-shared", "-fPIC", "-o", str(so), str(tmp_path / "recorder.cpp")], check=True)
+    code = textwrap.dedent(f"""
+        import ctypes, json, sys
+        R = ctypes.CDLL({str(so)!r}, ctypes.RTLD_GLOBAL)   # ahead of the runtime's own
+        sys.path.insert(0, {ROOT!r})
+        sys.path.insert(0, {os.path.join(ROOT, "tests")!r})
+        import collective_communication_primitives_coll_amd as coll
+        from test_token_abi_cpu import FarBufs, _i64
+        L, out = coll.lib(), (ctypes.c_uint * (6 * 65536))()
+        for call in {calls!r}:
+            b = FarBufs()
+            status = eval(call)
+            assert status == 0, (status, call)
+            n = R.launches(out)
+            assert 0 < n <= 65536, (n, call)
+            print(json.dumps([[out[6 * i:6 * i + 3], out[6 * i + 3:6 * i + 6]] for i in range(n)]))
+    """)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    found = [json.loads(line) for line in r.stdout.splitlines() if line.startswith("[[")]
+    assert len(found) == len(calls)
+    for call, launched in zip(calls, found):
+        for grid, block in launched:
+            assert all(g > 0 and g * w < 1 << 32 for g, w in zip(grid, block)), (call, grid, block)
+    return found
+
+
+@host_only
+def test_logprob_launches_hold_the_work_items_that_hip_takes(tmp_path):
+    shapes = [(64, 1 << 20, 1), (64, (1 << 20) + 3, 16), (1, 1 << 26, 8), (1, (1 << 28) + 1, 100), (8, 1 << 20, 16384), (1, 3, 0x7fffffff)]
+    calls = []
+    for p, rows, v in shapes:
+        one = f"_i64(*[{v}] * {p})"
+        calls.append(f"L.coll_vocab_logprob(b({p}), {one}, {one}, b.one(), 1.0, b({p}), b({p}), None, 0, None, None, {p}, {rows}, 1, "
+                     f"b.one(), coll.coll_vocab_logprob_workspace_bytes({rows}, [{v}] * {p}), None)")
+        calls.append(f"L.coll_vocab_logprob_backward(b({p}), {one}, {one}, b.one(), 1.0, b.one(), b.one(), None, None, b({p}), {one}, {p}, {rows}, 1, None)")
+    found = recorded(tmp_path, calls)
+    waves = lambda launched: sum(g[0] * b[0] // 64 for g, b in launched)  # noqa: E731
+    for (p, rows, v), fwd, back in zip(shapes, found[::2], found[1::2]):
+        assert waves(fwd) >= rows * p + rows and waves(back) >= rows * p * -(-v // 1024)       # pieces, then the join
