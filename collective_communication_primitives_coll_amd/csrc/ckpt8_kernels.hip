@@ -193,8 +193,8 @@ int launch_ckpt8(int kind, int dtype, Ckpt8Args a, int ranks, void* stream) {
   a.div_shift = 31 + sh;
   a.div_mul = ((uint64_t{1} << a.div_shift) + a.units - 1) / a.units;
   const uint64_t tile = kBlock * kCkptUnits, tiles = (a.rows * a.units + tile - 1) / tile;
-  const uint64_t cap = 0x1000000;
-  const dim3 grid((uint32_t)(tiles < cap ? tiles : cap), ranks), block(kBlock);
+  // (the workgroups walk what one launch cannot hold)
+  const dim3 grid((uint32_t)(tiles < most_blocks(kBlock) ? tiles : most_blocks(kBlock)), ranks), block(kBlock);
 #define COLL_CKPT8(K)                                                                                \
   if (dtype == kBF16) hipLaunchKernelGGL((K<kBF16, 8>), grid, block, 0, s, a);                       \
   else if (elems == 4) hipLaunchKernelGGL((K<kF32, 4>), grid, block, 0, s, a);                       \

@@ -401,3 +401,14 @@ def test_logprob_launches_hold_the_work_items_that_hip_takes(tmp_path):
     waves = lambda launched: sum(g[0] * b[0] // 64 for g, b in launched)  # noqa: E731
     for (p, rows, v), fwd, back in zip(shapes, found[::2], found[1::2]):
         assert waves(fwd) >= rows * p + rows and waves(back) >= rows * p * -(-v // 1024)       # pieces, then the join
+
+
+@host_only
+def test_checkpoint_launches_hold_the_work_items_that_hip_takes(tmp_path):
+    calls = []
+    for dt, rows in ((0, 1 << 22), (1, 1 << 22), (1, 1 << 23)):          # rows of 16384 elements: 2^24 tiles or more
+        calls += [f"L.coll_ckpt8_save(b(2), b(2), 2, {rows}, 16384, 128, {dt}, None)", f"L.coll_ckpt8_load(b(2), b(2), 2, {rows}, 16384, 128, {dt}, None)",
+                  f"L.coll_swiglu_ckpt8(b(2), b(2), b(2), 2, {rows}, 16384, 128, {dt}, None)",
+                  f"L.coll_swiglu_backward_ckpt8(b(2), b(2), b(2), b(2), 2, {rows}, 16384, 128, {dt}, None)"]
+    for launched in recorded(tmp_path, calls):
+        assert len(launched) == 1 and launched[0][0][1] == 2             # both ranks; the workgroups walk what the grid leaves
