@@ -630,7 +630,7 @@ template <int WT>
 __global__ __launch_bounds__(kJoinBlock) void ln_join_kernel(LnJoinArgs a) {
   __shared__ float sums[kJoinWays][kWave];
   const uint32_t col = threadIdx.x % kWave, way = threadIdx.x / kWave;
-  const uint64_t cols = 2 * a.hidden, j = (uint64_t)blockIdx.x * kWave + col;
+  const uint64_t cols = 2 * a.hidden, j = a.first + (uint64_t)blockIdx.x * kWave + col;
   float s = 0.0f;
   if (j < cols) {
     const float* w = as_global(a.ws) + j;
@@ -698,10 +698,24 @@ int with_shape(uint64_t hidden, F f) {
   return f(std::integral_constant<int, 1024>(), two);
 }
 
+// Workgroups that share a row's columns in the wide backward pass.
+uint64_t wide_chunks(uint64_t hidden) { return ((hidden + 7) / 8 + kBlock - 1) / kBlock; }
+
 bool is_wide(const LnArgs& a) {
   int tpr, nu;
   row_shape(a.hidden, &tpr, &nu);
   return !tpr;
+}
+
+// The forward pass's arguments n rows on.
+void skip_rows(LnArgs& a, uint64_t n, uint64_t row_bytes) {
+  for (int r = 0; r < a.ranks; ++r) {
+    a.x[r] = (const uint8_t*)a.x[r] + n * row_bytes;
+    a.y[r] = (uint8_t*)a.y[r] + n * row_bytes;
+    if (a.mean[r]) a.mean[r] += n;
+    if (a.rstd[r]) a.rstd[r] += n;
+    if (a.ckpt[r]) a.ckpt[r] += n * a.row_bytes;
+  }
 }
 
 template <int DT, int WT>
@@ -714,23 +728,28 @@ int forward_t(const LnArgs& a, bool ckpt, hipStream_t s) {
   }
   return with_shape(a.hidden, [&](auto T, auto N) {
     constexpr int TPR = decltype(T)::value, NU = decltype(N)::value * 8 / kElems<DT>, RPB = block_of(TPR) / TPR;
-    const uint64_t run = RPB * (ckpt ? rows_of<DT, TPR, true>() : rows_of<DT, TPR, false>()), runs = (a.rows + run - 1) / run;
-    if (runs > 0x7fffffffull) return (int)hipErrorInvalidConfiguration;
-    const dim3 grid((uint32_t)runs, a.ranks), block(block_of(TPR));
+    const uint64_t run = RPB * (ckpt ? rows_of<DT, TPR, true>() : rows_of<DT, TPR, false>());
+    const dim3 block(block_of(TPR));
     constexpr bool PACKED = TPR < kWave;  // several rows to a wave
-    if (ckpt) hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, PACKED, true>), grid, block, 0, s, a);
-    else if (PACKED || a.hidden % kElems<DT>) hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, true, false>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, PACKED, false>), grid, block, 0, s, a);
-    return (int)hipGetLastError();
+    const uint64_t most = most_blocks(block.x) * run;
+    LnArgs part = a;
+    for (uint64_t left = a.rows; left; skip_rows(part, part.rows, a.hidden * Traits<DT>::B)) {
+      part.rows = std::min(left, most);
+      left -= part.rows;
+      const dim3 grid((uint32_t)((part.rows + run - 1) / run), a.ranks);
+      if (ckpt) hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, PACKED, true>), grid, block, 0, s, part);
+      else if (PACKED || a.hidden % kElems<DT>) hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, true, false>), grid, block, 0, s, part);
+      else hipLaunchKernelGGL((ln_forward_kernel<DT, WT, TPR, NU, PACKED, false>), grid, block, 0, s, part);
+      if (const int e = (int)hipGetLastError()) return e;
+    }
+    return 0;
   });
 }
 
 template <int DT, int WT>
 int backward_t(const LnArgs& a, uint32_t groups, bool ckpt, hipStream_t s) {
   if (is_wide(a)) {
-    const uint64_t chunks = ((a.hidden + 7) / 8 + kBlock - 1) / kBlock;
-    if (chunks * groups > 0x7fffffffull) return (int)hipErrorInvalidConfiguration;
-    const dim3 cols((uint32_t)(chunks * groups)), rows((uint32_t)std::min<uint64_t>(a.rows, 65536), a.ranks);
+    const dim3 cols((uint32_t)(wide_chunks(a.hidden) * groups)), rows((uint32_t)std::min<uint64_t>(a.rows, 65536), a.ranks);
     if (ckpt) {
       hipLaunchKernelGGL((ln_backward_wide_columns_kernel<kE4M3, DT>), cols, dim3(kBlock), 0, s, a, groups);
       hipLaunchKernelGGL((ln_backward_wide_rows_kernel<kE4M3, DT, WT>), rows, dim3(1024), 0, s, a);
@@ -758,12 +777,13 @@ int backward_t(const LnArgs& a, uint32_t groups, bool ckpt, hipStream_t s) {
 // workgroup of 512 lanes to a CU: 8 x 4096 x 7168 bf16 took 238 us with 256,
 // 252 with 512 and 279 with 384, whose second round is short.  Two of 256
 // lanes or less: 3 x 1777 x 2565 fp32 took 39 us with 512, 42 with 768, which
-// write more partial sums, and 43.5 with 384.
+// write more partial sums, and 43.5 with 384.  In the wide form as many as one
+// launch over all columns may hold (fewer than 256 from 2^27 columns on).
 uint32_t ln_backward_groups(int p, uint64_t rows, uint64_t hidden) {
   int tpr, nu;
   row_shape(hidden, &tpr, &nu);
   const uint64_t rpb = tpr ? block_of(tpr) / tpr : 1, all = rows * (uint64_t)std::min(p, kArgRanks), need = (all + rpb - 1) / rpb;
-  const uint64_t most = tpr && tpr <= kBlock ? 512 : 256;
+  const uint64_t most = tpr && tpr <= kBlock ? 512 : tpr ? 256 : std::min<uint64_t>(256, most_blocks(kBlock) / wide_chunks(hidden));
   return (uint32_t)std::max<uint64_t>(1, std::min(need, most));
 }
 
@@ -787,12 +807,18 @@ int launch_ln_backward(int dtype, int wdtype, const LnArgs& a, uint32_t groups, 
   return wdtype == kF32 ? backward_t<kBF16, kF32>(a, groups, ckpt, s) : backward_t<kBF16, kBF16>(a, groups, ckpt, s);
 }
 
-int launch_ln_join(int wdtype, const LnJoinArgs& a, void* stream) {
+int launch_ln_join(int wdtype, const LnJoinArgs& args, void* stream) {
   hipStream_t s = (hipStream_t)stream;
-  const dim3 grid((uint32_t)((2 * a.hidden + kWave - 1) / kWave)), block(kJoinBlock);
-  if (wdtype == kF32) hipLaunchKernelGGL((ln_join_kernel<kF32>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((ln_join_kernel<kBF16>), grid, block, 0, s, a);
-  return (int)hipGetLastError();
+  LnJoinArgs a = args;
+  const uint64_t blocks = (2 * a.hidden + kWave - 1) / kWave, most = most_blocks(kJoinBlock);
+  for (uint64_t b = 0; b < blocks; b += most) {
+    a.first = b * kWave;
+    const dim3 grid((uint32_t)std::min(blocks - b, most)), block(kJoinBlock);
+    if (wdtype == kF32) hipLaunchKernelGGL((ln_join_kernel<kF32>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((ln_join_kernel<kBF16>), grid, block, 0, s, a);
+    if (const int e = (int)hipGetLastError()) return e;
+  }
+  return 0;
 }
 
 }  // namespace coll

@@ -39,6 +39,7 @@ struct LnJoinArgs {
   void* dbeta[kMaxRanks];
   const float* ws;               // [parts][2][hidden]
   uint64_t hidden;
+  uint64_t first;                // column of this launch's first sum, of 2 * hidden (set by the launcher)
   uint32_t parts;
   int p;
   int avg;

@@ -814,3 +814,55 @@ def test_logprob_of_more_rows_than_a_launch_holds(coll, p, rows):
         ge = prob.neg_().scatter_add_(1, tg[n, None], torch.ones_like(want)[:, None]).mul_(gl[n, None].double())
         got = torch.cat([x[n] for x in dz], 1).double()
         assert bool(((got - ge).abs() <= HALF[BF16] * ge.abs() + 300 * U * gl[n, None].double().abs()).all())
+
+
+def test_layernorm_of_more_rows_than_a_launch_holds(coll):
+    """Rows of 16 elements, 32 to a workgroup: a launch ends 32 rows short of 2^29, so the last rows take another one."""
+    import torch
+    g = rng(35)
+    hidden, rows, cut = 16, (1 << 29) + 5, (1 << 29) - 32
+    pick = [0, 1, 12345678, cut - 1, cut, cut + 1, cut + 31, rows - 2, rows - 1]
+    x = torch.zeros(rows, hidden, dtype=torch.bfloat16, device="cuda")
+    small, xe = dev(g.normal(0.5, 2, (len(pick), hidden)), BF16)
+    x[pick] = small
+    beta, be = dev(g.normal(0, 1, hidden), BF16)
+    gamma, ge = dev(g.normal(1, 0.3, hidden), BF16)
+    y = torch.full_like(x, float("nan"))
+    mean, rstd = f32(rows), f32(rows)
+    ck = u8(rows, coll.coll_ckpt8_row_bytes(hidden, 16))
+    coll.coll_layernorm_ckpt8([x], [gamma], [beta], [y], [mean], [rstd], [ck], hidden, 16)
+    torch.cuda.synchronize()
+    ye, me, re = token_ops.layernorm(xe, ge, be, 1e-5)
+    close(host(y[pick]), ye, ln_forward_tol(xe, ge, be, me, re, ye, BF16), "y")
+    close(host(mean[pick]), me, (chain(hidden) + 4) * U * np.abs(xe).mean(1), "mean")
+    close(host(rstd[pick]), re, re * ((chain(hidden) + 8) * U + re ** 2 * ((chain(hidden) + 4) * U * np.abs(xe).mean(1)) ** 2), "rstd")
+    assert np.array_equal(ck[pick].cpu().numpy(), token_ops.ckpt8_rows(xe.astype(np.float32), 16))
+    y[pick] = beta                                            # all others: rows of zeros
+    mean[pick] = 0.0
+    zeros = torch.from_numpy(token_ops.ckpt8_rows(np.zeros((1, hidden), dtype=np.float32), 16)).cuda()
+    ck[pick] = zeros
+    for a in range(0, rows, 1 << 26):
+        assert bool((y[a:a + (1 << 26)] == beta).all()) and bool((ck[a:a + (1 << 26)] == zeros).all()), a
+    assert bool((mean == 0).all())
+
+
+def test_layernorm_gradient_of_more_columns_than_a_launch_joins(coll):
+    """A row of 2^27 + 16 columns, whose weight gradients a join of 2^22 workgroups of 64 sums cannot hold."""
+    import torch
+    hidden = (1 << 27) + 16
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(36)
+    x, dy = [torch.randn(1, hidden, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    mean, rstd = torch.tensor([0.25], device="cuda"), torch.tensor([0.875], device="cuda")
+    dx, dg, db = torch.full_like(x, float("nan")), f32(hidden), f32(hidden)
+    ws = workspace(coll.coll_layernorm_workspace_bytes(1, 1, hidden))
+    coll.coll_layernorm_backward([dy], [x], [mean], [rstd], None, [dx], [dg], [db], ws, hidden, wdtype=F32)
+    torch.cuda.synchronize()
+    assert torch.equal(db, dy[0].float())                     # one row: nothing to add
+    n = (x[0].double() - 0.25) * 0.875
+    want = dy[0].double() * n
+    assert bool(((dg.double() - want).abs() <= 3 * U * want.abs() + TINY).all())
+    d = dy[0].double()
+    dxe = 0.875 * (d - d.mean() - n * want.mean())
+    # the two means: sums of 2^27 terms whose magnitudes are below 1 on average, 2^17 of them one after another in a lane
+    assert bool(((dx[0].double() - dxe).abs() <= HALF[BF16] * dxe.abs() + (chain(hidden) + 8) * U * (d.abs() + 1 + n.abs())).all())

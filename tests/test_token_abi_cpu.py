@@ -412,3 +412,29 @@ def test_checkpoint_launches_hold_the_work_items_that_hip_takes(tmp_path):
                   f"L.coll_swiglu_backward_ckpt8(b(2), b(2), b(2), b(2), 2, {rows}, 16384, 128, {dt}, None)"]
     for launched in recorded(tmp_path, calls):
         assert len(launched) == 1 and launched[0][0][1] == 2             # both ranks; the workgroups walk what the grid leaves
+
+
+@host_only
+def test_layernorm_launches_hold_the_work_items_that_hip_takes(tmp_path):
+    # rows of a few elements that need more than one launch of the forward pass; rows so wide that the backward
+    # pass's columns, or the join over them, do
+    forward = [(8, (1 << 29) - 32, 1), (8, 1 << 29, 2), (8, (1 << 31) + 7, 1), (300, (1 << 27) + 1, 1), (1024, 1 << 28, 1), (5120, 1 << 25, 2)]
+    calls = []
+    for h, rows, p in forward:
+        calls.append(f"L.coll_layernorm(b({p}), None, None, b({p}), b({p}), b({p}), {p}, {rows}, {h}, 1e-5, 1, 1, None)")
+        h = -(-h // 16) * 16
+        calls.append(f"L.coll_layernorm_ckpt8(b({p}), None, None, b({p}), b({p}), b({p}), b({p}), {p}, {rows}, {h}, 16, 1e-5, 0, 0, None)")
+    n_forward = len(calls)
+    backward = [(8, 1 << 30, 3), (1 << 27, 1, 1), ((1 << 27) + 9, 256, 2), (1 << 30, 64, 1), ((1 << 31) - 1, 200, 1)]
+    for h, rows, p in backward:
+        ws = f"b.one(), coll.coll_layernorm_workspace_bytes({p}, {rows}, {h}), None)"
+        calls.append(f"L.coll_layernorm_backward(b({p}), b({p}), b({p}), b({p}), None, b({p}), b({p}), b({p}), {p}, {rows}, {h}, 0, 1, 0, {ws}")
+        h = h // 16 * 16
+        calls.append(f"L.coll_layernorm_backward_ckpt8(b({p}), b({p}), b({p}), b({p}), None, None, b({p}), None, b({p}), b({p}), {p}, {rows}, "
+                     f"{max(h, 16)}, 16, 0, 1, 0, b.one(), coll.coll_layernorm_workspace_bytes({p}, {rows}, {max(h, 16)}), None)")
+    found = recorded(tmp_path, calls)
+    for (h, rows, p), launched in zip(forward, found[:n_forward:2]):
+        assert h > 8 or sum(g[0] for g, b in launched) * 32 >= rows      # 32 rows to a workgroup
+    for (h, rows, p), launched in zip(backward, found[n_forward::2]):
+        joins = launched[2 if h > 16384 else 1:]                         # after the columns and the rows, or both in one
+        assert sum(g[0] for g, b in joins) * 64 >= 2 * h, (h, launched)
