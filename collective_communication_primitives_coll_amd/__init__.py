@@ -889,7 +889,8 @@ def _targets(targets, rows: int | None):
 
 
 def coll_vocab_logprob_workspace_bytes(rows: int, vocab: Sequence[int], top_k: int = 0) -> int:
-    """Workspace of coll_vocab_logprob; vocab lists every rank's shard."""
+    """Workspace of coll_vocab_logprob for up to `rows` rows; vocab lists every
+    rank's shard."""
     return int(lib().coll_vocab_logprob_workspace_bytes(len(vocab), int(rows), _i64_array(vocab), int(top_k)))
 
 

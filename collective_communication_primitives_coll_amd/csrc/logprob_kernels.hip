@@ -771,17 +771,14 @@ int pieces_of(int64_t vocab, int64_t before, int64_t len) { return vocab ? (int)
 
 }  // namespace
 
-// Pieces of a wave's step or more: enough for some 8192 waves
-// over all rows, and none over 32768 elements, as far as a row's 64 pieces
-// allow.
+// Pieces of a wave's step or more: as many as wanted, and none over 32768
+// elements, as far as a row's 64 pieces allow.
 void logprob_plan(int p, uint64_t rows, const int64_t* vocab, LogprobPlan* plan) {
-  const int64_t unit = kLogprobStep, most = kMaxPieces / p, most_before = kLine / 2 - 1;
-  // (rows past 8192 want one piece as 8192 do; their product with p may not fit)
-  const uint64_t shards = std::min<uint64_t>(rows, 8192) * (uint64_t)p, want = shards ? (8192 + shards - 1) / shards : 1;
+  const int64_t unit = kLogprobStep, most = kMaxPieces / p, most_before = kLine / 2 - 1, want = (int64_t)logprob_want(p, rows);
   plan->first[0] = 0;
   for (int r = 0; r < p; ++r) {
     const int64_t v = vocab[r] + most_before;
-    int64_t s = std::min<int64_t>(most, std::max<int64_t>((int64_t)std::min<uint64_t>(want, 64), (v + 32767) / 32768));
+    int64_t s = std::min<int64_t>(most, std::max<int64_t>(want, (v + 32767) / 32768));
     s = std::max<int64_t>(1, std::min<int64_t>(s, (v + unit - 1) / unit));
     const int64_t len = ((v + s - 1) / s + 511) / 512 * 512;
     plan->len[r] = len;

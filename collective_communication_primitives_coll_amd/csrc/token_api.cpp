@@ -290,6 +290,13 @@ size_t shard_bytes(size_t rows, int64_t ld, int64_t vocab, size_t d) {
   return vocab ? ((rows - 1) * (size_t)ld + (size_t)vocab) * d : 0;
 }
 
+// Workspace bytes of one call with so many rows.
+bool logprob_need(int p, size_t rows, const int64_t* vocab, int top_k, size_t* bytes) {
+  coll::LogprobPlan plan;
+  coll::logprob_plan(p, rows, vocab, &plan);
+  return mul_ok(rows, (size_t)plan.pieces, coll::logprob_piece_bytes(plan, top_k), bytes);
+}
+
 }  // namespace
 
 COLL_EXPORT coll_status_t coll_layernorm(const void* const* x, const void* const* gamma, const void* const* beta,
@@ -415,10 +422,17 @@ COLL_EXPORT size_t coll_vocab_logprob_workspace_bytes(int p, size_t rows, const 
   if (p < 1 || p > kMaxRanks || !vocab || top_k < 0 || top_k > coll::kMaxTop) return 0;
   for (int r = 0; r < p; ++r)
     if (vocab[r] < 0 || vocab[r] > 0x7fffffffll) return 0;
-  coll::LogprobPlan plan;
-  coll::logprob_plan(p, rows, vocab, &plan);
-  size_t bytes;
-  return mul_ok(rows, (size_t)plan.pieces, coll::logprob_piece_bytes(plan, top_k), &bytes) ? bytes : 0;
+  // Fewer rows are cut into more pieces, which may take more: the most that
+  // any number of rows up to this one needs.  It grows with the rows as long
+  // as these want one number of pieces, so the last of each such run decides.
+  size_t most;
+  if (!logprob_need(p, rows, vocab, top_k, &most)) return 0;
+  for (uint64_t want = 2; want <= coll::kMaxPieces; ++want) {
+    const uint64_t last = coll::logprob_most_rows(p, want);
+    size_t bytes;
+    if (last < rows && logprob_need(p, last, vocab, top_k, &bytes)) most = std::max(most, bytes);
+  }
+  return most;
 }
 
 COLL_EXPORT coll_status_t coll_vocab_logprob(const void* const* logits, const int64_t* ld, const int64_t* vocab,

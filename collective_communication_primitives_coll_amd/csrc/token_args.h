@@ -71,6 +71,17 @@ constexpr int kLogprobStep = 2048;
 // Groups of elements (a row's) whose largest the search for alternatives
 // starts from.  Eight lanes, so whole 128-byte lines, share a group.
 constexpr int kMaxGroups = 1024, kGroupLanes = 8, kSegGroups = 64 / kGroupLanes;
+// Pieces that a shard's row is cut into, as far as its length allows: enough
+// for kLogprobWaves waves over all rows.  (Rows past that many want one piece;
+// their product with p may not fit.)
+constexpr uint64_t kLogprobWaves = 8192;
+inline uint64_t logprob_want(int p, uint64_t rows) {
+  const uint64_t shards = (rows < kLogprobWaves ? rows : kLogprobWaves) * (uint64_t)p;
+  const uint64_t want = shards ? (kLogprobWaves + shards - 1) / shards : 1;
+  return want < kMaxPieces ? want : kMaxPieces;
+}
+// The most rows that want so many (2 or more).
+inline uint64_t logprob_most_rows(int p, uint64_t want) { return (kLogprobWaves - 1) / ((want - 1) * (uint64_t)p); }
 struct LogprobPlan {
   int pieces;                    // per row, over all ranks
   uint64_t ranks_q32;            // ranks to a piece on average, times 2^32: where a piece's rank is first sought

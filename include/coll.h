@@ -457,7 +457,8 @@ coll_status_t coll_layernorm(const void* const* x, const void* const* gamma, con
  * COLL_ERR_UNSUPPORTED).  Every rank gets the total: dgamma[r], dbeta[r]
  * hold `hidden` elements of wdtype, each array optional.  mean and rstd are
  * those of the forward pass.  workspace: device memory of at least
- * coll_layernorm_workspace_bytes(p, rows, hidden) bytes, 16-byte aligned.
+ * coll_layernorm_workspace_bytes(p, rows, hidden) bytes, 16-byte aligned
+ * (they serve every smaller number of rows too).
  * In place: dx[r] == dy[r].  rows == 0 writes zeros to dgamma and dbeta. */
 coll_status_t coll_layernorm_backward(const void* const* dy, const void* const* x, const float* const* mean,
                                       const float* const* rstd, const void* const* gamma, void* const* dx,
@@ -539,7 +540,8 @@ coll_status_t coll_swiglu_backward_ckpt8(const void* const* ckpt, const void* co
  * nothing else: m = L = logp = -inf, entropy 0, gradient 0.  A row that holds
  * a NaN or +infinity: NaN throughout, alternatives -1.
  * workspace: coll_vocab_logprob_workspace_bytes(p, rows, vocab, top_k)
- * bytes, 16-byte aligned.  rows == 0 is a no-op. */
+ * bytes, 16-byte aligned; as many serve every smaller number of rows too.
+ * rows == 0 is a no-op. */
 coll_status_t coll_vocab_logprob(const void* const* logits, const int64_t* ld, const int64_t* vocab,
                                  const int64_t* targets, float inv_temp, float* const* stats, float* const* logp,
                                  float* const* entropy, int top_k, float* const* top_logp, int32_t* const* top_idx,

@@ -866,3 +866,20 @@ def test_layernorm_gradient_of_more_columns_than_a_launch_joins(coll):
     dxe = 0.875 * (d - d.mean() - n * want.mean())
     # the two means: sums of 2^27 terms whose magnitudes are below 1 on average, 2^17 of them one after another in a lane
     assert bool(((dx[0].double() - dxe).abs() <= HALF[BF16] * dxe.abs() + (chain(hidden) + 8) * U * (d.abs() + 1 + n.abs())).all())
+
+
+def test_logprob_in_a_workspace_for_more_rows(coll):
+    """4095 rows of 6200 entries, cut into three pieces each, in the workspace of 4096, which need two each."""
+    import torch
+    g = rng(37)
+    rows, v, top = 4095, 6200, 4
+    zs, ze = shards(g.normal(0, 3, (rows, v)), [0, v], BF16)
+    targets = [int(x) for x in g.integers(0, v, rows)]
+    tg = torch.tensor(targets, dtype=torch.int64, device="cuda")
+    o = {"stats": f32(1, rows, 2), "logp": f32(1, rows), "entropy": f32(1, rows), "top_logp": f32(1, rows, top),
+         "top_idx": torch.full((1, rows, top), -7, dtype=torch.int32, device="cuda")}
+    ws = workspace(coll.coll_vocab_logprob_workspace_bytes(rows + 1, [v], top))
+    coll.coll_vocab_logprob(zs, tg, list(o["stats"]), list(o["logp"]), ws, entropy=list(o["entropy"]), top_k=top,
+                            top_logp=list(o["top_logp"]), top_idx=list(o["top_idx"]))
+    torch.cuda.synchronize()
+    check_logprob(o, token_ops.logprob(ze, targets, 1.0, top), targets, 1.0, top)

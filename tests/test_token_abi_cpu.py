@@ -438,3 +438,31 @@ def test_layernorm_launches_hold_the_work_items_that_hip_takes(tmp_path):
     for (h, rows, p), launched in zip(backward, found[n_forward::2]):
         joins = launched[2 if h > 16384 else 1:]                         # after the columns and the rows, or both in one
         assert sum(g[0] for g, b in joins) * 64 >= 2 * h, (h, launched)
+
+
+LOGPROB_VOCABS = [[16384] * 8, [131072], [50257], [1], [2000, 70000, 0], [12564, 12564, 12564, 12565], [1000] * 64, [100000] * 5]
+
+
+def test_workspaces_never_shrink_as_rows_grow():
+    for vocab in LOGPROB_VOCABS:
+        for top in (0, 1, 8, 32):
+            had = 0
+            for rows in [*range(0, 2100), *range(2100, 9000, 97), 1 << 20, (1 << 20) + 1, 1 << 40]:
+                n = coll.coll_vocab_logprob_workspace_bytes(rows, vocab, top)
+                assert n >= had and (n > 0) == (rows > 0), (vocab, top, rows)
+                had = n
+    for p, hidden in [(1, 7), (8, 64), (3, 2565), (33, 7168), (64, 20000)]:
+        sizes = [coll.coll_layernorm_workspace_bytes(p, rows, hidden) for rows in range(0, 3000, 7)]
+        assert sizes == sorted(sizes) and sizes[0] > 0, (p, hidden)
+
+
+@host_only
+def test_a_workspace_for_more_rows_serves_fewer(tmp_path):
+    calls = []
+    for vocab in LOGPROB_VOCABS:
+        p, ld = len(vocab), [max(v, 1) for v in vocab]
+        for rows, most in ((1000, 1024), (1023, 1024), (1, 2), (500, 8192), (63, 200), (129, 130), (4095, 4096)):
+            for top in (0, 8):
+                calls.append(f"L.coll_vocab_logprob(b({p}), _i64(*{ld}), _i64(*{vocab}), b.one(), 1.0, b({p}), b({p}), None, {top}, b({p}), b({p}), "
+                             f"{p}, {rows}, 1, b.one(), coll.coll_vocab_logprob_workspace_bytes({most}, {vocab}, {top}), None)")
+    recorded(tmp_path, calls)
