@@ -674,7 +674,9 @@ def _wdtype_of(lists, wdtype: int | None, dt: int) -> int:
 
 
 def _rows_of(x, hidden: int, rows: int | None) -> int:
-    return int(rows) if rows is not None else _numel(x, None) // int(hidden)
+    if rows is not None:
+        return int(rows)
+    return _numel(x, None) // int(hidden) if hidden else 0
 
 
 def _layernorm(fname, x, gamma, beta, y, mean, rstd, ckpt, hidden, group, eps, rows, dtype, wdtype, stream, defer):

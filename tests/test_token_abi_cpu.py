@@ -466,3 +466,17 @@ def test_a_workspace_for_more_rows_serves_fewer(tmp_path):
                 calls.append(f"L.coll_vocab_logprob(b({p}), _i64(*{ld}), _i64(*{vocab}), b.one(), 1.0, b({p}), b({p}), None, {top}, b({p}), b({p}), "
                              f"{p}, {rows}, 1, b.one(), coll.coll_vocab_logprob_workspace_bytes({most}, {vocab}, {top}), None)")
     recorded(tmp_path, calls)
+
+
+def test_rows_without_columns_are_refused_by_the_library():
+    """The binding counts rows where they are not given; no columns are the library's to refuse."""
+    import torch
+    f, u = lambda *s: [DeviceTensor(torch.float32, *s)], lambda *s: [DeviceTensor(torch.uint8, *s)]  # noqa: E731
+    for call in (lambda: coll.coll_layernorm(f(4, 8), None, None, f(4, 8), 0, stream=0),
+                 lambda: coll.coll_layernorm_backward(f(4, 8), f(4, 8), f(4), f(4), None, f(4, 8), None, None, f(64)[0], 0, stream=0),
+                 lambda: coll.coll_ckpt8_save(f(4, 8), u(64), 0, 16, stream=0), lambda: coll.coll_ckpt8_load(u(64), f(4, 8), 0, 16, stream=0),
+                 lambda: coll.coll_swiglu_ckpt8(f(4, 8), f(4, 4), u(64), 0, 16, stream=0),
+                 lambda: coll.coll_swiglu_backward_ckpt8(u(64), f(4, 4), f(4, 8), 0, 16, stream=0)):
+        with pytest.raises(coll.CollError) as e:
+            call()
+        assert e.value.status == INV
