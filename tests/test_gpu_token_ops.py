@@ -261,6 +261,42 @@ def test_layernorm_gradient_by_differences(coll):
             assert abs((loss(x, *a) - loss(x, *b)) / step - host(got[0])[j]) < lim
 
 
+@pytest.mark.parametrize("dtype,wdtype", [(F32, F32), (BF16, BF16), (BF16, F32)])
+@pytest.mark.parametrize("hidden", [8, 64, 320, 1024, 2560, 4096, 7168, 12288, 16384, 16400])
+def test_layernorm_of_whole_units_off_their_boundary(coll, hidden, dtype, wdtype):
+    """Widths of whole 16-byte units whose every buffer starts at an element's address only: the same bits as from
+    aligned buffers."""
+    import torch
+    g = rng(22, hidden, dtype, wdtype)
+    rows, group = 5, 16
+    data = [g.normal(0.5, 2, (rows, hidden)), g.normal(0, 1, (rows, hidden)), g.normal(1, 0.3, hidden), g.normal(0, 0.5, hidden)]
+    got = []
+    for off in (0, 1, 3):
+        x, dy, gamma, beta = [dev(a, t, off)[0] for a, t in zip(data, (dtype, dtype, wdtype, wdtype))]
+        if off:
+            assert all(t.data_ptr() % 16 for t in (x, dy, gamma, beta))
+        y, dx, y2, dx2, again = [new((rows, hidden), dtype, off) for _ in range(5)]
+        dg, db, dg2, db2 = [new((hidden,), wdtype, off) for _ in range(4)]
+        mean, rstd = f32(rows), f32(rows)
+        ws = workspace(coll.coll_layernorm_workspace_bytes(1, rows, hidden))
+        coll.coll_layernorm([x], [gamma], [beta], [y], hidden, mean=[mean], rstd=[rstd])
+        coll.coll_layernorm_backward([dy], [x], [mean], [rstd], [gamma], [dx], [dg], [db], ws, hidden)
+        out = [y, mean, rstd, dx, dg, db]
+        if hidden % group == 0:
+            ck = u8(rows, coll.coll_ckpt8_row_bytes(hidden, group))
+            coll.coll_layernorm_ckpt8([x], [gamma], [beta], [y2], [mean], [rstd], [ck], hidden, group)
+            coll.coll_layernorm_backward_ckpt8([dy], [ck], [mean], [rstd], [gamma], [dx2], [dg2], [db2], ws, hidden, group, beta=[beta], y=[again])
+            out += [y2, ck, dx2, dg2, db2, again]
+        torch.cuda.synchronize()
+        got.append([t.clone() for t in out])
+        for t in (y, dx, dg, db):                              # nothing past the end
+            assert torch.isnan(t.view(-1).as_strided((1,), (1,), t.storage_offset() + t.numel()).float()).all()
+    assert not torch.isnan(got[0][0].float()).any() and not torch.isnan(got[0][3].float()).any()
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("hidden", [7, 9, 136, 320, 1000, 1800, 2560, 3001, 4608, 7168, 9000, 12296, 20003])
 def test_layernorm_gradient_of_a_large_constant_row(coll, hidden, dtype):
