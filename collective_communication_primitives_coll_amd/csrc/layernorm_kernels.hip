@@ -162,9 +162,10 @@ __device__ __forceinline__ uint64_t own_row(uint64_t block) {
 // (5.4 TB/s), bound by how many rows the registers hold.  The codes are
 // stored in the first pass: 116-119 us after it, 115 us with the results.
 // ---------------------------------------------------------------------------
-// Rows to a lane: one where two workgroups of 1024 lanes then fit a CU (bf16
-// without checkpoints: 8 x 2048 x 16384 179 us instead of 213; with them 255
-// and 249, in fp32 199 and 180, since their registers leave room for one).
+// Rows to a lane: one where two workgroups of 1024 lanes then fit a CU, which
+// bf16 without checkpoints does.  8 x 2048 x 16384, one row and two, in us: 179
+// and 213; with checkpoints and fp32 weights 269 and 249 (bf16 weights 242 and
+// 249); fp32 391 and 348, with checkpoints 417 and 404.
 template <int DT, int TPR, bool CKPT>
 constexpr int rows_of() { return TPR == 1024 && DT == kBF16 && !CKPT ? 1 : 2; }
 

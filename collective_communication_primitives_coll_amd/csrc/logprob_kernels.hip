@@ -27,6 +27,11 @@
 // 2048 rows of 131072 bf16: 88 us without alternatives, 102 us with 8, of
 // which the join takes 4 and 10: one wave's chain of loads, searches and
 // stores, as long for 4 rows (15 us in all) as for 2048.
+// A row of fewer than k groups has no such bound (8 groups to 2048 entries of
+// a shard where there are many rows: up to 4096 entries with 20 alternatives,
+// up to 6144 with 32).  Every unmasked element then counts as reaching it, and
+// from 257 of them on the row is searched again, by insertion.  8192 rows of
+// 4000 bf16 in one shard: 21 us without alternatives, 37 with 8, 80 with 20.
 // (Insertion into a sorted list while the chunks came took 120 us; a search
 // in each piece, whose end no other work hides, 127 us; groups of one lane's
 // elements over a whole piece, each in a line of its own, 110 us.)
@@ -56,7 +61,8 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 constexpr float kFar = -16384.0f;
 // Where the sums take one fma an element for its difference to the maximum:
-// eps, at most 2^-25 of m c, is then small enough to be taken back out.
+// eps, at most 2^-24 of |m c|, is then at most 2^-5 (|m c| stays below 2^20),
+// small enough to be taken back out with a factor near 1.
 constexpr float kPlainMax = 1e4f, kPlainScale = 100.0f;
 constexpr int kStep = kLogprobStep / kWave;  // elements per lane and step
 
@@ -214,7 +220,8 @@ __device__ __forceinline__ int reached_by(float y, float mine) {
   if constexpr (N < 15) return one + reached_by<N + 1>(y, mine);
   return one;
 }
-// A bound that at least `top` lanes reach (or that all unmasked elements do).
+// A bound that at least `top` lanes reach (or that all unmasked elements do,
+// where fewer lanes have a group with any).
 __device__ __forceinline__ float bar_of(float mine, int top) {
   // the wave's four rows of 16 lanes, each on all rows
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(mine), __float_as_uint(mine), false, false);
@@ -538,7 +545,8 @@ __device__ __forceinline__ unsigned long long row_best(const JoinInput& a, uint6
     wave_fence();
   } else {
     // more ties with the bar, or more of the best in few lanes, than there
-    // is room for: the whole row again, by insertion
+    // is room for, or no bar in too few groups: the whole row again, by
+    // insertion
     TopList list;
     for (int i = 0; i < a.pieces; ++i) {
       u32x4 at;
