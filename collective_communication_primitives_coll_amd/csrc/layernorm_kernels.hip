@@ -587,7 +587,8 @@ __global__ __launch_bounds__(1024) void ln_backward_wide_rows_kernel(LnArgs a) {
 #pragma unroll
       for (uint32_t e = 0; e < 8; ++e) {
         // past the row's end zero, not -mean rstd, which may be infinite
-        n[e] = u < full || e < part ? (n[e] - mean) * rstd : 0.0f;
+        // (checkpoint rows are whole units)
+        n[e] = SRC == kE4M3 || u < full || e < part ? (n[e] - mean) * rstd : 0.0f;
         w[e] *= g[e];
       }
     };
