@@ -48,23 +48,16 @@
 // Gradient: 4 bytes an element in bf16, read once and written once.  4096 x
 // 65536 bf16 in 8 shards: 171 us, 6.28 TB/s, what a stream read and written
 // one to one reaches on this card.
-#include <float.h>
-
-#include <algorithm>
-
-#include "token_unit.h"
+#include "vocab_pieces.h"
 
 namespace coll {
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
-constexpr float kFar = -16384.0f;
 // Where the sums take one fma an element for its difference to the maximum:
 // eps, at most 2^-24 of |m c|, is then at most 2^-5 (|m c| stays below 2^20),
 // small enough to be taken back out with a factor near 1.
 constexpr float kPlainMax = 1e4f, kPlainScale = 100.0f;
-constexpr int kStep = kLogprobStep / kWave;  // elements per lane and step
 
 // The order of fp32 values as unsigned integers (both zeros alike).
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -137,57 +130,6 @@ struct TopList {
   }
 };
 
-// A piece of a row's shard: its elements before the first 16-byte boundary,
-// its whole units and the rest.  Pieces after the first start on a 128-byte
-// line, so that no two waves share one and only a shard's two ends go element
-// by element.
-constexpr int kLine = 128;
-struct Piece {
-  int64_t begin;       // first element
-  uint32_t head, tail; // elements
-  uint32_t units;      // of 16 bytes
-};
-template <int DT>
-__device__ __forceinline__ Piece piece_of(const uint8_t* row, int64_t vocab, int64_t len, int k) {
-  constexpr int B = Traits<DT>::B, E = kElems<DT>;
-  const int64_t mis = (int64_t)((uintptr_t)row % kLine) / B;
-  Piece c;
-  c.begin = k ? (int64_t)k * len - mis : 0;
-  int64_t end = (int64_t)(k + 1) * len - mis;
-  if (c.begin > vocab) c.begin = vocab;
-  if (end > vocab) end = vocab;
-  const uint32_t n = (uint32_t)(end - c.begin);
-  const uint32_t h = (uint32_t)(((16 - (((uintptr_t)row + c.begin * B) & 15)) & 15) / B);
-  c.head = h < n ? h : n;
-  c.units = (n - c.head) / E;
-  c.tail = n - c.head - c.units * E;
-  return c;
-}
-
-// A launch's item: a piece of a row.  No loop over items, so that nothing is
-// hoisted out of it, and 32-bit numbers within a launch.
-struct Item {
-  uint64_t row;
-  int piece, r;  // of the row, rank that holds it
-  bool any;
-  __device__ __forceinline__ Item(const LogprobPlan& plan, uint64_t rows, uint64_t first_row, int p) {
-    const uint32_t i = blockIdx.x * (kBlock / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t in = i / (uint32_t)plan.pieces;
-    row = first_row + in;
-    any = in < rows;
-    piece = (int)(i - in * (uint32_t)plan.pieces);
-    r = min((int)((2 * (uint64_t)piece + 1) * plan.ranks_q32 >> 33), p - 1);
-    while (plan.first[r] > piece) --r;
-    while (plan.first[r + 1] <= piece) ++r;
-  }
-};
-
-template <int DT>
-__device__ __forceinline__ RawUnit<DT, kElems<DT>> masked_unit() {
-  const uint32_t w = DT == kBF16 ? 0xff80ff80u : 0xff800000u;
-  return RawUnit<DT, kElems<DT>>{{u32x4{w, w, w, w}}};
-}
-
 // A lane's running maximum m (raw), S = sum 2^d and A = sum 2^d d about it.
 struct Running {
   float m = -FLT_MAX, s = 0.0f, a = 0.0f;
@@ -204,14 +146,6 @@ struct Running {
     a = wave_sum(a);
   }
 };
-
-template <int N>
-__device__ __forceinline__ float largest(const float (&f)[N]) {
-  float v = f[0];
-#pragma unroll
-  for (int e = 1; e < N; ++e) v = fmaxf(v, f[e]);
-  return v;
-}
 
 // How many of a row's 16 values, each lane's row of 16, reach `mine`.
 template <int N = 0>
@@ -265,14 +199,6 @@ struct JoinStore {
   unsigned long long keys[kBagMost];
   unsigned long long sorted[kMaxTop];
 };
-
-template <int N>
-__device__ __forceinline__ float sum_of(const float (&v)[N]) {
-  float s = v[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) s += v[i];
-  return s;
-}
 
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kBlock) void logprob_pieces_kernel(LogprobArgs a) {
@@ -752,30 +678,6 @@ __global__ __launch_bounds__(kBlock) void logprob_grad_kernel(LogprobGradArgs a,
     }
   }
 }
-
-uint32_t wave_grid(uint64_t waves) { return (uint32_t)((waves + kBlock / kWave - 1) / (kBlock / kWave)); }
-
-// Calls f(first row, rows, blocks) for launches of as many rows as one may
-// have, `waves` waves to a row (2^22 at most, so that a row always fits).
-template <class F>
-int over_rows(uint64_t rows, uint64_t waves, F f) {
-  const uint64_t most = most_blocks(kBlock) * (kBlock / kWave) / waves;
-  for (uint64_t first = 0; first < rows; first += most) {
-    const uint64_t n = std::min(most, rows - first);
-    f(first, n, dim3(wave_grid(n * waves)));
-    if (const int e = (int)hipGetLastError()) return e;
-  }
-  return 0;
-}
-
-void finish_plan(LogprobPlan* plan, int p) {
-  plan->pieces = plan->first[p];
-  plan->ranks_q32 = ((uint64_t)p << 32) / (uint64_t)std::max(plan->pieces, 1);
-}
-
-// Pieces of `len` elements that cover a shard whose rows start at most
-// `before` elements after a line's start.
-int pieces_of(int64_t vocab, int64_t before, int64_t len) { return vocab ? (int)((vocab + before + len - 1) / len) : 0; }
 
 }  // namespace
 
