@@ -97,6 +97,9 @@ def lib() -> ctypes.CDLL:
         "coll_layernorm_backward": [pp, pp, pp, pp, pp, pp, pp, pp, i32, sz, sz, i32, i32, i32, vp, sz, vp],
         "coll_layernorm_backward_ckpt8": [pp, pp, pp, pp, pp, pp, pp, pp, pp, pp, i32, sz, sz, sz, i32, i32, i32, vp,
                                           sz, vp],
+        "coll_rmsnorm": [pp, pp, pp, pp, pp, pp, i32, sz, sz, f32, i32, i32, vp],
+        "coll_rmsnorm_fp8": [pp, pp, pp, pp, pp, pp, pp, i32, sz, sz, sz, f32, i32, i32, vp],
+        "coll_rmsnorm_backward": [pp, pp, pp, pp, pp, pp, pp, i32, sz, sz, i32, i32, i32, vp, sz, vp],
         "coll_ckpt8_save": [pp, pp, i32, sz, sz, sz, i32, vp],
         "coll_ckpt8_load": [pp, pp, i32, sz, sz, sz, i32, vp],
         "coll_swiglu_ckpt8": [pp, pp, pp, i32, sz, sz, sz, i32, vp],
@@ -119,6 +122,8 @@ def lib() -> ctypes.CDLL:
     L.coll_moe_fp8_row_bytes.restype = sz
     L.coll_layernorm_workspace_bytes.argtypes = [i32, sz, sz]
     L.coll_layernorm_workspace_bytes.restype = sz
+    L.coll_rmsnorm_workspace_bytes.argtypes = [i32, sz, sz]
+    L.coll_rmsnorm_workspace_bytes.restype = sz
     L.coll_ckpt8_row_bytes.argtypes = [sz, sz]
     L.coll_ckpt8_row_bytes.restype = sz
     L.coll_vocab_logprob_workspace_bytes.argtypes = [i32, sz, i64p, i32]
@@ -663,6 +668,13 @@ def _f32(what: str, *lists) -> None:
                 raise ValueError(f"{what} must be float32")
 
 
+def _u8(what: str, xs) -> None:
+    import torch
+    for x in xs:
+        if hasattr(x, "dtype") and x.dtype != torch.uint8:
+            raise ValueError(f"{what} must be uint8")
+
+
 def _wdtype_of(lists, wdtype: int | None, dt: int) -> int:
     """The weights' type: given, or that of the first weight listed, else dt."""
     have = [xs for xs in lists if xs is not None]
@@ -781,6 +793,80 @@ def coll_layernorm_backward_ckpt8(dy, ckpt, mean, rstd, gamma, dx, dgamma, dbeta
     gets the forward's output again (beta is only needed for it)."""
     return _layernorm_backward("coll_layernorm_backward_ckpt8", dy, ckpt, mean, rstd, gamma, beta, dx, y, dgamma, dbeta,
                                workspace, hidden, int(group), op, rows, dtype, wdtype, workspace_bytes, stream, defer)
+
+
+def _rmsnorm(fname, x, residual, gamma, h, y, rstd, y8, hidden, group, eps, rows, dtype, wdtype, stream, defer):
+    p = len(x)
+    _same_ranks(p, residual, gamma, h, y, rstd, y8)
+    dt = _dtype_of(x[0], dtype)
+    data = [t for ts in (x, residual, h, y) for t in ts or []]
+    _same_dtype(data, dt)
+    wt = _wdtype_of([gamma], wdtype, dt)
+    rows = _rows_of(x[0], hidden, rows)
+    _check_sizes(data, rows * hidden, fname)
+    _check_sizes(gamma or [], hidden, fname + " weights")
+    _check_sizes(rstd or [], rows, fname + " rstd")
+    _f32(fname + " rstd", rstd)
+    arrays = [_ptr_array(x), _opt_array(residual), _opt_array(gamma), _opt_array(h), _opt_array(y), _opt_array(rstd)]
+    shape = (p, rows, int(hidden))
+    if y8 is not None:
+        _u8(fname + " y8", y8)
+        _check_sizes(y8, rows * coll_ckpt8_row_bytes(hidden, group), fname + " y8")
+        arrays.append(_ptr_array(y8))
+        shape += (int(group),)
+    return _run(fname, (*[a for a, _ in arrays], *shape, float(eps), dt, wt, _stream(stream)), fname, defer,
+                tuple(k for _, k in arrays))
+
+
+def coll_rmsnorm(x, gamma, y, hidden: int, eps: float = 1e-6, residual=None, h=None, rstd=None,
+                 rows: int | None = None, dtype: int | None = None, wdtype: int | None = None, stream=None,
+                 defer: bool = False):
+    """RMS norm of each rank's rows [rows*hidden], of x + residual where a
+    residual is listed; h (or None) gets that sum.  gamma (or None) lists every
+    rank's copy; rstd (or None) fp32 [rows]."""
+    return _rmsnorm("coll_rmsnorm", x, residual, gamma, h, y, rstd, None, hidden, 0, eps, rows, dtype, wdtype, stream,
+                    defer)
+
+
+def coll_rmsnorm_fp8(x, gamma, y8, hidden: int, group: int, eps: float = 1e-6, residual=None, h=None, rstd=None, y=None,
+                     rows: int | None = None, dtype: int | None = None, wdtype: int | None = None, stream=None,
+                     defer: bool = False):
+    """coll_rmsnorm with its output in 8 bits: y8 uint8
+    [rows * coll_ckpt8_row_bytes(hidden, group)]; y (or None) gets it too."""
+    if y8 is None:
+        raise ValueError("y8 lists the buffers of the 8-bit rows")
+    return _rmsnorm("coll_rmsnorm_fp8", x, residual, gamma, h, y, rstd, y8, hidden, group, eps, rows, dtype, wdtype,
+                    stream, defer)
+
+
+def coll_rmsnorm_workspace_bytes(p: int, rows: int, hidden: int) -> int:
+    return int(lib().coll_rmsnorm_workspace_bytes(int(p), int(rows), int(hidden)))
+
+
+def coll_rmsnorm_backward(dy, h, rstd, gamma, dx, dgamma, workspace, hidden: int, op: int = COLL_SUM, dh=None,
+                          rows: int | None = None, dtype: int | None = None, wdtype: int | None = None,
+                          workspace_bytes: int | None = None, stream=None, defer: bool = False):
+    """dx of each rank's rows, plus dh (or None), the gradient that reaches h by
+    the residual stream; dgamma (or None), summed or averaged (op) over all rows
+    of all ranks, goes to every rank.  workspace: a device buffer of
+    coll_rmsnorm_workspace_bytes(p, rows, hidden)."""
+    fname = "coll_rmsnorm_backward"
+    p = len(dy)
+    _same_ranks(p, h, rstd, gamma, dx, dgamma, dh)
+    dt = _dtype_of(dy[0], dtype)
+    data = [t for ts in (dy, h, dx, dh) for t in ts or []]
+    _same_dtype(data, dt)
+    wt = _wdtype_of([gamma, dgamma], wdtype, dt)
+    rows = _rows_of(dy[0], hidden, rows)
+    _check_sizes(data, rows * hidden, fname)
+    _check_sizes([t for ts in (gamma, dgamma) for t in ts or []], hidden, fname + " weights")
+    _check_sizes(rstd, rows, fname + " rstd")
+    _f32(fname + " rstd", rstd)
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    arrays = [_ptr_array(dy), _opt_array(dh), _ptr_array(h), _ptr_array(rstd), _opt_array(gamma), _ptr_array(dx),
+              _opt_array(dgamma)]
+    return _run(fname, (*[a for a, _ in arrays], p, rows, int(hidden), int(op), dt, wt, ws, nbytes, _stream(stream)),
+                fname, defer, (*[k for _, k in arrays], workspace))
 
 
 def coll_ckpt8_row_bytes(hidden: int, group: int) -> int:

@@ -34,6 +34,7 @@ SOURCES = [
     "moe_kernels.hip",
     "fp8_kernels.hip",
     "layernorm_kernels.hip",
+    "rmsnorm_kernels.hip",
     "ckpt8_kernels.hip",
     "logprob_kernels.hip",
     "probe_kernels.hip",

@@ -484,7 +484,7 @@ template <int WT>
 __global__ __launch_bounds__(kJoinBlock) void ln_join_kernel(LnJoinArgs a) {
   __shared__ float sums[kJoinWays][kWave];
   const uint32_t col = threadIdx.x % kWave, way = threadIdx.x / kWave;
-  const uint64_t cols = 2 * a.hidden, j = a.first + (uint64_t)blockIdx.x * kWave + col;
+  const uint64_t cols = a.sums * a.hidden, j = a.first + (uint64_t)blockIdx.x * kWave + col;
   float s = 0.0f;
   if (j < cols) {
     const float* w = as_global(a.ws) + j;
@@ -621,7 +621,7 @@ int launch_ln_backward(int dtype, int wdtype, const LnArgs& a, uint32_t groups, 
 int launch_ln_join(int wdtype, const LnJoinArgs& args, void* stream) {
   hipStream_t s = (hipStream_t)stream;
   LnJoinArgs a = args;
-  const uint64_t blocks = (2 * a.hidden + kWave - 1) / kWave, most = most_blocks(kJoinBlock);
+  const uint64_t blocks = (a.sums * a.hidden + kWave - 1) / kWave, most = most_blocks(kJoinBlock);
   for (uint64_t b = 0; b < blocks; b += most) {
     a.first = b * kWave;
     const dim3 grid((uint32_t)std::min(blocks - b, most)), block(kJoinBlock);

@@ -1,0 +1,544 @@
+// RMS norm over every rank's token rows, with the residual's addition before
+// it and an output in the rows' type or in 8 bits, and its backward pass with
+// the weights' gradient summed over all rows and all ranks.
+//
+//   forward   h = x + residual (rounded to the rows' type: the next layer and
+//             the backward pass see the same h),
+//             r = 1 / sqrt(mean h^2 + eps),  y = h r gamma
+//   backward  n = h r,  w = dy gamma,
+//             dx = r (w - n mean(w n)) + dh,
+//             dgamma = sum dy n   (over rows and ranks)
+//
+// Bound by HBM: 8 bytes an element either way in bf16 with a residual,
+// against some 10 fp32 operations.  As in layer norm, a row is read once and
+// stays in the registers of TPR lanes between its sum and its result, and the
+// backward pass keeps a lane on the same columns for all rows of its
+// workgroup; the partial sums of the weights' gradient are added in a fixed
+// order by the norms' common join.
+//
+// Sums are fp32; bf16 results are narrowed once, 8-bit codes come from the
+// fp32 values.  Squares leave fp32's range long before the values do: a row
+// whose sum of squares is out of it (or, with eps next to nothing, far below
+// it) is summed again with its values scaled by a power of two.
+#include "token_rows.h"
+
+namespace coll {
+
+namespace {
+
+// Sums of squares that are taken as they are; others again, scaled: by 2^-80,
+// which brings values below 2^48 and 2^31 of their squares below 2^127, or by
+// 2^100, which brings the smallest denormal to 2^-49.  eps above 2^-80
+// outweighs any sum below kLeast, and is not scaled out of range below it.
+constexpr float kMost = 0x1p120f, kLeast = 0x1p-90f, kDown = 0x1p-80f, kUp = 0x1p100f, kEpsLeast = 0x1p-80f;
+__device__ __forceinline__ float square_scale(float q, float eps) {
+  return !(q < kMost) ? kDown : q < kLeast && eps < kEpsLeast ? kUp : 1.0f;
+}
+// 1 / sqrt(mean h^2 + eps) from the sum of (h k)^2.
+__device__ __forceinline__ float rstd_of(float q, float k, float hidden, float eps) {
+  return rsqrtf(q / hidden + eps * k * k) * k;
+}
+
+template <int DT, int E>
+__device__ __forceinline__ RawUnit<DT, E> add_units(const RawUnit<DT, E>& a, const RawUnit<DT, E>& b) {
+  float f[E], g[E];
+  widen_unit(a, f);
+  widen_unit(b, g);
+#pragma unroll
+  for (int e = 0; e < E; ++e) f[e] += g[e];
+  return narrow_unit<DT, E>(f);
+}
+
+// ---------------------------------------------------------------------------
+// Forward.  Grid (runs of rows, ranks), no walk, two rows to a lane, and the
+// weights asked for after the sums, as in layer norm.  h is stored after the
+// sums too: it may replace x or the residual, whose rows of an odd width have
+// lanes that share elements.
+// ---------------------------------------------------------------------------
+template <int DT, int TPR>
+constexpr int rows_of() { return TPR == 1024 && DT == kBF16 ? 1 : 2; }
+
+template <int DT, int WT, int TPR, int NU, bool TAIL, bool RES, bool FP8>
+__global__ __launch_bounds__(block_of(TPR)) void rms_forward_kernel(RmsArgs a) {
+  constexpr int E = kElems<DT>;
+  constexpr int kRows = rows_of<DT, TPR>();
+  __shared__ float red[2][kRows][waves_of(TPR)];
+  const int rank = blockIdx.y;
+  const uint32_t lane = threadIdx.x % TPR, H = (uint32_t)a.hidden;
+  const uint64_t row_bytes = (uint64_t)H * Traits<DT>::B;
+  const uint64_t row0 = own_row<TPR>(blockIdx.x) * kRows;
+  if (row0 >= a.rows) return;
+  RawUnit<DT, E> raw[kRows][NU], res[kRows][NU];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    // past the last row: row0 again (its results are not stored)
+    const uint64_t off = (row0 + (row0 + k < a.rows ? k : 0)) * row_bytes;
+    const Row<DT, E, TAIL> x(static_cast<const uint8_t*>(a.x[rank]) + off, H);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) raw[k][i] = x.template get<true>(i * TPR + lane);
+    if constexpr (RES) {
+      const Row<DT, E, TAIL> r(static_cast<const uint8_t*>(a.res[rank]) + off, H);
+#pragma unroll
+      for (int i = 0; i < NU; ++i) res[k][i] = r.template get<true>(i * TPR + lane);
+    }
+  }
+  // sum of squares of row k, the values times `by`
+  auto squares = [&](int k, float by) {
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const uint32_t skip = TAIL && may_end<TPR, NU>(i) ? skip_of<E>(i * TPR + lane, H) : 0;
+      float f[E];
+      widen_unit(raw[k][i], f);
+#pragma unroll
+      for (uint32_t e = 0; e < E; ++e) {
+        const float v = f[e] * by;
+        q = TAIL && may_end<TPR, NU>(i) && e < skip ? q : __builtin_fmaf(v, v, q);
+      }
+    }
+    return q;
+  };
+  float q[kRows], by[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if constexpr (RES) {
+#pragma unroll
+      for (int i = 0; i < NU; ++i) raw[k][i] = add_units<DT, E>(raw[k][i], res[k][i]);
+    }
+    q[k] = squares(k, 1.0f);
+  }
+  row_sums<TPR, kRows>(q, red[0]);
+  bool scaled = false;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    by[k] = square_scale(q[k], a.eps);
+    scaled = scaled || by[k] != 1.0f;
+  }
+  if (scaled) {  // the same on all lanes of the rows
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) q[k] = squares(k, by[k]);
+    row_sums<TPR, kRows>(q, red[1]);
+  }
+  RawUnit<WT, E> gamma[NU];
+  load_weights<WT, E, TAIL, NU, TPR>(a.gamma[rank], 1.0f, lane, H, gamma);
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const uint64_t row = row0 + k;
+    if (row >= a.rows) break;
+    const float rstd = rstd_of(q[k], by[k], (float)H, a.eps);
+    if (RES && a.h[rank]) {
+      const Row<DT, E, TAIL> h(static_cast<uint8_t*>(a.h[rank]) + row * row_bytes, H);
+#pragma unroll
+      for (int i = 0; i < NU; ++i) h.template put<true>(i * TPR + lane, raw[k][i]);
+    }
+    uint8_t* y8 = FP8 ? a.y8[rank] + row * a.row_bytes : nullptr;
+    // (of a row to itself; where a wave holds several, by their addresses)
+    const RowBuffer codes(y8, FP8 ? H : 0), scales(FP8 ? y8 + H : nullptr, FP8 ? (H >> a.glog) * 4 : 0);
+    const bool plain = !FP8 || a.y[rank];
+    const Row<DT, E, TAIL> y(static_cast<uint8_t*>(a.y[rank]) + row * row_bytes, H);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      float f[E], g[E];
+      widen_unit(raw[k][i], f);
+      widen_unit(gamma[i], g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f[e] = f[e] * rstd * g[e];
+      if (plain) y.template put<true>(i * TPR + lane, narrow_unit<DT, E>(f));
+      if constexpr (FP8) {
+        const uint32_t u = i * TPR + lane;
+        const RawUnit<kE4M3, E> code = encode_values<E>(f, a.glog);
+        if constexpr (TPR >= kWave) store_codes<E, true>(codes, scales, E * u, a.glog, code);
+        else if (E * u < H) store_codes<E, true>(y8, H, a.row_bytes, E * u, a.glog, code);
+      }
+    }
+    if constexpr (FP8 && TPR >= kWave) pad_codes(y8, H, a.row_bytes, a.glog, lane);
+    if (lane == 0 && a.rstd[rank]) as_global(a.rstd[rank])[row] = rstd;
+  }
+}
+
+// Rows too wide for the registers (or narrower than one unit): units of 8
+// elements in every type, each row gone over twice; the second time it comes
+// from the caches.
+template <int DT, int WT, bool RES, bool FP8>
+__global__ __launch_bounds__(1024) void rms_forward_wide_kernel(RmsArgs a) {
+  constexpr int TPR = 1024;
+  __shared__ float red[2][1][TPR / kWave];
+  const int rank = blockIdx.y;
+  const uint64_t H = a.hidden, full = H / 8, units = (H + 7) / 8;
+  const uint32_t part = (uint32_t)(H % 8);
+  // every lane takes part in every step (the encoding exchanges lanes)
+  const uint64_t steps = (units + TPR - 1) / TPR;
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const uint64_t off = row * H * Traits<DT>::B;
+    const uint8_t* x = static_cast<const uint8_t*>(a.x[rank]) + off;
+    const uint8_t* res = RES ? static_cast<const uint8_t*>(a.res[rank]) + off : nullptr;
+    uint8_t* h = RES && a.h[rank] ? static_cast<uint8_t*>(a.h[rank]) + off : nullptr;
+    uint8_t* y = !FP8 || a.y[rank] ? static_cast<uint8_t*>(a.y[rank]) + off : nullptr;
+    uint8_t* y8 = FP8 ? a.y8[rank] + row * a.row_bytes : nullptr;
+    float f[8], q[1] = {0.0f};
+    // a unit of h: from x and the residual, or, once it is stored, read back
+    // (x may have been replaced by it)
+    auto unit = [&](uint64_t u, bool again) {
+      if (RES && again && h) {
+        widen_unit(row_unit<DT>(h, u, full, part), f);
+        return;
+      }
+      RawUnit<DT, 8> v = row_unit<DT>(x, u, full, part);
+      if constexpr (RES) v = add_units<DT, 8>(v, row_unit<DT>(res, u, full, part));
+      widen_unit(v, f);
+    };
+    for (uint64_t k = 0; k < steps; ++k) {
+      const uint64_t u = k * TPR + threadIdx.x;
+      unit(u, false);
+      if (RES && h) put_unit<DT>(h, u, full, part, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[0] = __builtin_fmaf(f[e], f[e], q[0]);
+    }
+    row_sums<TPR, 1>(q, red[0]);
+    const float by = square_scale(q[0], a.eps);
+    if (by != 1.0f) {
+      q[0] = 0.0f;
+      for (uint64_t k = 0; k < steps; ++k) {
+        unit(k * TPR + threadIdx.x, true);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[0] = __builtin_fmaf(f[e] * by, f[e] * by, q[0]);
+      }
+    }
+    // a barrier either way: a wave that writes red[0] for the next row has
+    // passed one that every wave reached after reading it
+    float s[1] = {q[0]};
+    if (by != 1.0f) row_sums<TPR, 1>(s, red[1]);
+    else __syncthreads();
+    const float rstd = rstd_of(s[0], by, (float)H, a.eps);
+    for (uint64_t k = 0; k < steps; ++k) {
+      const uint64_t u = k * TPR + threadIdx.x;
+      unit(u, true);
+      float g[8];
+      weight_unit<WT>(a.gamma[rank], 1.0f, u, full, part, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
+      if (y) put_unit<DT>(y, u, full, part, f);
+      if constexpr (FP8) {
+        const RawUnit<kE4M3, 8> code = encode_values<8>(f, a.glog);
+        if (u < full) store_codes<8, true>(y8, H, a.row_bytes, u * 8, a.glog, code);
+      }
+    }
+    if (threadIdx.x == 0 && a.rstd[rank]) as_global(a.rstd[rank])[row] = rstd;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward.  A workgroup takes every gridDim.x-th run of rows, through all
+// ranks of the launch, and writes its partial sums to ws[blockIdx.x][hidden].
+// ---------------------------------------------------------------------------
+template <int DT, int WT, int TPR, int NU, bool TAIL, bool DH>
+__global__ __launch_bounds__(block_of(TPR)) void rms_backward_kernel(RmsArgs a) {
+  constexpr int E = kElems<DT>, RPB = block_of(TPR) / TPR, AHEAD = kAhead<TPR>;
+  __shared__ float red[2][1][waves_of(TPR)];
+  __shared__ float fold[RPB > 1 ? NU * E * TPR : 1];
+  const uint32_t lane = threadIdx.x % TPR, H = (uint32_t)a.hidden;
+  const uint64_t row_bytes = (uint64_t)H * Traits<DT>::B;
+  const uint64_t stride = (uint64_t)gridDim.x * RPB;
+  // a place in the ranks' rows, one rank after the other
+  struct Place {
+    uint64_t row;
+    int rank;
+    __device__ __forceinline__ void settle(const RmsArgs& a) {
+      while (row >= a.rows && rank < a.ranks) {
+        row -= a.rows;
+        ++rank;
+      }
+    }
+  };
+  Place at{own_row<TPR>(blockIdx.x), 0};
+  at.settle(a);
+  float dg[NU][E] = {};
+  if (at.rank < a.ranks) {
+    // AHEAD + 1 buffers; the loop is unrolled over them, since moving a
+    // loaded register to another waits for its load
+    RawUnit<DT, E> bh[AHEAD + 1][NU], bd[AHEAD + 1][NU], br[AHEAD + 1][DH ? NU : 1];
+    float bs[AHEAD + 1];
+    auto fetch = [&](const Place& r, auto K) {
+      constexpr int k = decltype(K)::value;
+      const uint64_t off = r.row * row_bytes;
+      const Row<DT, E, TAIL> rh(static_cast<const uint8_t*>(a.h[r.rank]) + off, H);
+      const Row<DT, E, TAIL> rd(static_cast<const uint8_t*>(a.x[r.rank]) + off, H);
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        bh[k][i] = rh.template get<true>(i * TPR + lane);
+        bd[k][i] = rd.template get<true>(i * TPR + lane);
+      }
+      if constexpr (DH) {
+        const Row<DT, E, TAIL> rr(static_cast<const uint8_t*>(a.res[r.rank]) + off, H);
+#pragma unroll
+        for (int i = 0; i < NU; ++i) br[k][i] = rr.template get<true>(i * TPR + lane);
+      }
+      bs[k] = ld_const(a.rstd[r.rank] + r.row);
+    };
+    fetch(at, std::integral_constant<int, 0>());
+    RawUnit<WT, E> gamma[NU];
+    int held = -1, turn = 0;
+    // one row from buffer K; whether there is another
+    auto step = [&](auto K) {
+      constexpr int k = decltype(K)::value;
+      if (at.rank != held) {
+        held = at.rank;
+        load_weights<WT, E, TAIL, NU, TPR>(a.gamma[held], 1.0f, lane, H, gamma);
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (auto& v : gamma[i].v) asm volatile("" : "+v"(v));  // waited for here, not in every step
+      }
+      // after the last row: that row again, so that every step issues the
+      // same and the compiler can count what it waits for
+      Place next{at.row + stride, at.rank};
+      next.settle(a);
+      const bool more = next.rank < a.ranks;
+      if (!more) next = at;
+      if constexpr (AHEAD > 0) fetch(next, std::integral_constant<int, (k + 1) % (AHEAD + 1)>());
+      const float rstd = bs[k];
+      float n[NU][E], w[NU][E], s[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        const uint32_t skip = TAIL && may_end<TPR, NU>(i) ? skip_of<E>(i * TPR + lane, H) : 0;
+        float d[E], g[E];
+        widen_unit(bh[k][i], n[i]);
+        widen_unit(bd[k][i], d);
+        widen_unit(gamma[i], g);
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e) {
+          n[i][e] *= rstd;
+          w[i][e] = d[e] * g[e];
+          const bool own = !(TAIL && may_end<TPR, NU>(i) && e < skip);
+          dg[i][e] += own ? d[e] * n[i][e] : 0.0f;
+          s[0] += own ? w[i][e] * n[i][e] : 0.0f;
+        }
+      }
+      row_sums<TPR, 1>(s, red[turn]);
+      turn ^= 1;
+      const float c = s[0] / (float)H;
+      const Row<DT, E, TAIL> dx(static_cast<uint8_t*>(a.y[at.rank]) + at.row * row_bytes, H);
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        float r[E];
+        if constexpr (DH) widen_unit(br[k][i], r);
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[i][e] = rstd * (w[i][e] - n[i][e] * c) + (DH ? r[e] : 0.0f);
+        dx.template put<true>(i * TPR + lane, narrow_unit<DT, E>(w[i]));
+      }
+      if constexpr (AHEAD == 0) fetch(next, K);
+      at = next;
+      return more;
+    };
+    while (true) {
+      if (!step(std::integral_constant<int, 0>())) break;
+      if constexpr (AHEAD > 0)
+        if (!step(std::integral_constant<int, 1>())) break;
+    }
+  }
+  float* ws = a.ws + (uint64_t)blockIdx.x * H;
+  if constexpr (RPB > 1) {
+    // the workgroup's groups of lanes add their sums in turn
+    const int mine = (int)own_row<TPR>(0);
+    for (int k = 0; k < RPB; ++k) {
+      if (mine == k) {
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            float* to = fold + (i * E + e) * TPR + lane;
+            dg[i][e] += k ? to[0] : 0.0f;
+            to[0] = dg[i][e];
+          }
+      }
+      __syncthreads();
+    }
+    if (mine != RPB - 1) return;
+  }
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const uint32_t u = i * TPR + lane;
+    if (E * u + E <= H) {
+      store_unit<kF32, E, false>((void*)ws, E * u, narrow_unit<kF32, E>(dg[i]));
+    } else if (TAIL && E * u < H) {
+      // the row's last E elements, of which the last H % E are this unit's
+      const uint32_t skip = skip_of<E>(u, H);
+#pragma unroll
+      for (uint32_t e = 0; e < E; ++e)
+        if (e >= skip) as_global(ws)[H - E + e] = dg[i][e];
+    }
+  }
+}
+
+// Rows too wide for the registers, in two kernels: the weights' gradient by
+// columns (a lane keeps its 8 columns over the workgroup's rows), then the
+// rows, each gone over twice.  The columns come first, so that dx may be
+// dy's own buffer.
+template <int DT>
+__global__ __launch_bounds__(kBlock) void rms_backward_wide_columns_kernel(RmsArgs a, uint32_t splits) {
+  const uint64_t H = a.hidden, full = H / 8, row_bytes = H * Traits<DT>::B;
+  const uint32_t part = (uint32_t)(H % 8), split = blockIdx.x % splits;
+  const uint64_t u = (uint64_t)(blockIdx.x / splits) * kBlock + threadIdx.x;
+  float dg[8] = {};
+  for (int rank = 0; rank < a.ranks; ++rank)
+    for (uint64_t row = split; row < a.rows; row += splits) {
+      float fh[8], fd[8];
+      widen_unit(row_unit<DT>(static_cast<const uint8_t*>(a.h[rank]) + row * row_bytes, u, full, part), fh);
+      widen_unit(row_unit<DT>(static_cast<const uint8_t*>(a.x[rank]) + row * row_bytes, u, full, part), fd);
+      const float rstd = as_global(a.rstd[rank])[row];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dg[e] += fd[e] * (fh[e] * rstd);
+    }
+  put_unit<kF32>(a.ws + (uint64_t)split * H, u, full, part, dg);
+}
+
+template <int DT, int WT, bool DH>
+__global__ __launch_bounds__(1024) void rms_backward_wide_rows_kernel(RmsArgs a) {
+  constexpr int TPR = 1024;
+  __shared__ float red[2][1][TPR / kWave];
+  const int rank = blockIdx.y;
+  const uint64_t H = a.hidden, full = H / 8, units = (H + 7) / 8;
+  const uint32_t part = (uint32_t)(H % 8);
+  int turn = 0;
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const uint64_t off = row * H * Traits<DT>::B;
+    const uint8_t* h = static_cast<const uint8_t*>(a.h[rank]) + off;
+    const uint8_t* dy = static_cast<const uint8_t*>(a.x[rank]) + off;
+    const float rstd = as_global(a.rstd[rank])[row];
+    float n[8], w[8], g[8], s[1] = {0.0f};
+    auto unit = [&](uint64_t u) {
+      widen_unit(row_unit<DT>(h, u, full, part), n);
+      widen_unit(row_unit<DT>(dy, u, full, part), w);
+      weight_unit<WT>(a.gamma[rank], 1.0f, u, full, part, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[e] *= rstd;
+        w[e] *= g[e];
+      }
+    };
+    for (uint64_t u = threadIdx.x; u < units; u += TPR) {
+      unit(u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[0] += w[e] * n[e];
+    }
+    row_sums<TPR, 1>(s, red[turn]);
+    turn ^= 1;
+    const float c = s[0] / (float)H;
+    for (uint64_t u = threadIdx.x; u < units; u += TPR) {
+      unit(u);
+      float r[8] = {};
+      if constexpr (DH) widen_unit(row_unit<DT>(static_cast<const uint8_t*>(a.res[rank]) + off, u, full, part), r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = rstd * (w[e] - n[e] * c) + r[e];
+      put_unit<DT>(static_cast<uint8_t*>(a.y[rank]) + off, u, full, part, w);
+    }
+  }
+}
+
+// The kernel that takes rows of a width: lanes to a row and units to a lane
+// (0: the wide ones).  Codes want a group's lanes in one run of a row's, at
+// most a wave: rows of 16 lanes take 64 for wider groups, and fp32 rows of
+// groups of 512 the wide kernel, whose lanes hold 8 elements in every type.
+void rms_shape(int dtype, uint64_t hidden, uint64_t group, int* tpr, int* nu) {
+  row_shape(hidden, tpr, nu);
+  const uint64_t elems = dtype == kF32 ? 4 : 8;
+  if (*tpr == 16 && group > 16 * elems) {
+    *tpr = 64;
+    *nu = 1;
+  }
+  if (group > kWave * elems) *tpr = 0;
+}
+
+// The forward pass's arguments n rows on.
+void skip_rows(RmsArgs& a, uint64_t n, uint64_t row_bytes) {
+  for (int r = 0; r < a.ranks; ++r) {
+    a.x[r] = (const uint8_t*)a.x[r] + n * row_bytes;
+    if (a.res[r]) a.res[r] = (const uint8_t*)a.res[r] + n * row_bytes;
+    if (a.h[r]) a.h[r] = (uint8_t*)a.h[r] + n * row_bytes;
+    if (a.y[r]) a.y[r] = (uint8_t*)a.y[r] + n * row_bytes;
+    if (a.rstd[r]) a.rstd[r] += n;
+    if (a.y8[r]) a.y8[r] += n * a.row_bytes;
+  }
+}
+
+template <int DT, int WT, bool RES, bool FP8>
+int forward_t(const RmsArgs& a, hipStream_t s) {
+  int tpr, nu;
+  rms_shape(DT, a.hidden, FP8 ? uint64_t{1} << a.glog : 0, &tpr, &nu);
+  if (!tpr) {
+    const dim3 grid((uint32_t)std::min<uint64_t>(a.rows, 65536), a.ranks);
+    hipLaunchKernelGGL((rms_forward_wide_kernel<DT, WT, RES, FP8>), grid, dim3(1024), 0, s, a);
+    return (int)hipGetLastError();
+  }
+  return with_shape(tpr, nu, [&](auto T, auto N) {
+    constexpr int TPR = decltype(T)::value, NU = decltype(N)::value * 8 / kElems<DT>, RPB = block_of(TPR) / TPR;
+    constexpr bool PACKED = TPR < kWave;  // several rows to a wave
+    const uint64_t run = RPB * rows_of<DT, TPR>();
+    const dim3 block(block_of(TPR));
+    const uint64_t most = most_blocks(block.x) * run;
+    RmsArgs part = a;
+    for (uint64_t left = a.rows; left; skip_rows(part, part.rows, a.hidden * Traits<DT>::B)) {
+      part.rows = std::min(left, most);
+      left -= part.rows;
+      const dim3 grid((uint32_t)((part.rows + run - 1) / run), a.ranks);
+      if constexpr (FP8) {  // whole groups, so whole units
+        hipLaunchKernelGGL((rms_forward_kernel<DT, WT, TPR, NU, PACKED, RES, true>), grid, block, 0, s, part);
+      } else {
+        if (PACKED || a.hidden % kElems<DT>) hipLaunchKernelGGL((rms_forward_kernel<DT, WT, TPR, NU, true, RES, false>), grid, block, 0, s, part);
+        else hipLaunchKernelGGL((rms_forward_kernel<DT, WT, TPR, NU, PACKED, RES, false>), grid, block, 0, s, part);
+      }
+      if (const int e = (int)hipGetLastError()) return e;
+    }
+    return 0;
+  });
+}
+
+template <int DT, int WT, bool DH>
+int backward_t(const RmsArgs& a, uint32_t groups, hipStream_t s) {
+  int tpr, nu;
+  row_shape(a.hidden, &tpr, &nu);
+  if (!tpr) {
+    const dim3 cols((uint32_t)(wide_chunks(a.hidden) * groups)), rows((uint32_t)std::min<uint64_t>(a.rows, 65536), a.ranks);
+    hipLaunchKernelGGL((rms_backward_wide_columns_kernel<DT>), cols, dim3(kBlock), 0, s, a, groups);
+    hipLaunchKernelGGL((rms_backward_wide_rows_kernel<DT, WT, DH>), rows, dim3(1024), 0, s, a);
+    return (int)hipGetLastError();
+  }
+  return with_shape(tpr, nu, [&](auto T, auto N) {
+    constexpr int TPR = decltype(T)::value, NU = decltype(N)::value * 8 / kElems<DT>;
+    constexpr bool PACKED = TPR < kWave;
+    const dim3 grid(groups), block(block_of(TPR));
+    if (PACKED || a.hidden % kElems<DT>) hipLaunchKernelGGL((rms_backward_kernel<DT, WT, TPR, NU, true, DH>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((rms_backward_kernel<DT, WT, TPR, NU, PACKED, DH>), grid, block, 0, s, a);
+    return (int)hipGetLastError();
+  });
+}
+
+template <int DT, int WT>
+int forward_w(const RmsArgs& a, bool residual, bool fp8, hipStream_t s) {
+  if (residual) return fp8 ? forward_t<DT, WT, true, true>(a, s) : forward_t<DT, WT, true, false>(a, s);
+  return fp8 ? forward_t<DT, WT, false, true>(a, s) : forward_t<DT, WT, false, false>(a, s);
+}
+template <int DT, int WT>
+int backward_w(const RmsArgs& a, bool dh, uint32_t groups, hipStream_t s) {
+  return dh ? backward_t<DT, WT, true>(a, groups, s) : backward_t<DT, WT, false>(a, groups, s);
+}
+
+}  // namespace
+
+// Workgroups of a launch of the backward pass: by the shape alone (results
+// and workspace must not depend on the device or on the grid limit).
+uint32_t rms_backward_groups(int p, uint64_t rows, uint64_t hidden) { return ln_backward_groups(p, rows, hidden); }
+
+int launch_rms_forward(int dtype, int wdtype, const RmsArgs& a, bool residual, bool fp8, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  if (dtype == kF32) return forward_w<kF32, kF32>(a, residual, fp8, s);
+  return wdtype == kF32 ? forward_w<kBF16, kF32>(a, residual, fp8, s) : forward_w<kBF16, kBF16>(a, residual, fp8, s);
+}
+
+int launch_rms_backward(int dtype, int wdtype, const RmsArgs& a, bool dh, uint32_t groups, void* stream) {
+  hipStream_t s = (hipStream_t)stream;
+  if (dtype == kF32) return backward_w<kF32, kF32>(a, dh, groups, s);
+  return wdtype == kF32 ? backward_w<kBF16, kF32>(a, dh, groups, s) : backward_w<kBF16, kBF16>(a, dh, groups, s);
+}
+
+}  // namespace coll

@@ -1,5 +1,5 @@
-// Host side of the token-wise operators' entry points: layer norm, 8-bit
-// checkpoints, vocabulary log probabilities.  Argument checks, byte ranges
+// Host side of the token-wise operators' entry points: layer norm, RMS norm,
+// 8-bit checkpoints, vocabulary log probabilities.  Argument checks, byte ranges
 // and the record of the last HIP error are internal to coll_api.cpp, so that
 // file is part of this translation unit, and is not compiled by itself.
 #include "coll_api.cpp"
@@ -245,10 +245,71 @@ coll_status_t ln_backward(const void* const* dy, const void* const* x, bool from
   }
   j.ws = (const float*)workspace;
   j.hidden = hidden;
+  j.sums = 2;
   j.parts = rows ? (uint32_t)ln_launches(p) * groups : 0;  // no rows: the sums are zero
   j.p = p;
   j.avg = op == COLL_AVG;
   return finish(coll::launch_ln_join(wdtype, j, stream));
+}
+
+coll_status_t rms_forward(const void* const* x, const void* const* residual, const void* const* gamma, void* const* h,
+                          void* const* y, float* const* rstd, void* const* y8, bool fp8, int p, size_t rows,
+                          size_t hidden, size_t group, float eps, int dtype, int wdtype, void* stream) {
+  size_t bytes, bytes8;
+  coll_status_t st = check_ln_shape(p, rows, hidden, group, fp8, dtype, wdtype, &bytes, &bytes8);
+  if (st != COLL_OK) return st;
+  if (!(eps >= 0.0f) || eps > 3e38f || (h && !residual)) return COLL_ERR_INVALID_ARG;
+  if (rows == 0) return COLL_OK;
+  if (!all_non_null(x, p) || !none_or_all(residual, p) || !none_or_all(gamma, p) || !none_or_all(h, p) ||
+      (fp8 ? !all_non_null(y8, p) || !none_or_all(y, p) : !all_non_null(y, p)) || !none_or_all(rstd, p))
+    return COLL_ERR_INVALID_ARG;
+  const size_t d = dsize(dtype), w = dsize(wdtype);
+  if (!elem_aligned(x, p, d) || !aligned_or_none(residual, p, d) || !aligned_or_none(gamma, p, w) ||
+      !aligned_or_none(h, p, d) || !aligned_or_none(y, p, d) || !aligned_or_none(rstd, p, 4) ||
+      (fp8 && !elem_aligned(y8, p, 16)))
+    return COLL_ERR_INVALID_ARG;
+  RangeSet rs;
+  for (int r = 0; r < p; ++r) {
+    // h and y may each take the place of their rank's x or residual
+    const void* in[2] = {x[r], residual ? residual[r] : nullptr};
+    for (const void* q : in)
+      if (!(h && q == h[r]) && !(y && q == y[r])) rs.add(q, bytes, false);
+  }
+  rs.add_all(h, p, bytes, true);
+  rs.add_all(y, p, bytes, true);
+  rs.add_all(gamma, p, hidden * w, false);
+  rs.add_all(rstd, p, rows * 4, true);
+  if (fp8) rs.add_all(y8, p, bytes8, true);
+  st = rs.check();
+  if (st != COLL_OK) return st;
+  for (int r0 = 0; r0 < p; r0 += coll::kArgRanks) {
+    const int n = std::min(p - r0, coll::kArgRanks);
+    coll::RmsArgs a{};
+    for (int r = 0; r < n; ++r) {
+      a.x[r] = x[r0 + r];
+      if (residual) a.res[r] = residual[r0 + r];
+      if (gamma) a.gamma[r] = gamma[r0 + r];
+      if (h) a.h[r] = h[r0 + r];
+      if (y) a.y[r] = y[r0 + r];
+      if (rstd) a.rstd[r] = rstd[r0 + r];
+      if (fp8) a.y8[r] = (uint8_t*)y8[r0 + r];
+    }
+    a.rows = rows;
+    a.hidden = hidden;
+    a.ranks = n;
+    a.eps = eps;
+    if (fp8) {
+      a.row_bytes = fp8_row_bytes(hidden, group);
+      a.glog = group_log(group);
+    }
+    const int e = coll::launch_rms_forward(dtype, wdtype, a, residual != nullptr, fp8, stream);
+    if (e) return hip_fail(e);
+  }
+  return COLL_OK;
+}
+
+size_t rms_workspace(int p, size_t rows, size_t hidden) {
+  return (size_t)ln_launches(p) * coll::rms_backward_groups(p, rows, hidden) * hidden * sizeof(float);
 }
 
 // Shards of a vocabulary: sizes, strides and the first index of each.
@@ -338,6 +399,90 @@ COLL_EXPORT coll_status_t coll_layernorm_backward_ckpt8(const void* const* dy, c
                                                         void* stream) {
   return ln_backward(dy, ckpt, true, mean, rstd, gamma, beta, dx, y, dgamma, dbeta, p, rows, hidden, group, op, dtype,
                      wdtype, workspace, workspace_bytes, stream);
+}
+
+COLL_EXPORT coll_status_t coll_rmsnorm(const void* const* x, const void* const* residual, const void* const* gamma,
+                                       void* const* h, void* const* y, float* const* rstd, int p, size_t rows,
+                                       size_t hidden, float eps, coll_dtype_t dtype, coll_dtype_t wdtype, void* stream) {
+  return rms_forward(x, residual, gamma, h, y, rstd, nullptr, false, p, rows, hidden, 0, eps, dtype, wdtype, stream);
+}
+
+COLL_EXPORT coll_status_t coll_rmsnorm_fp8(const void* const* x, const void* const* residual, const void* const* gamma,
+                                           void* const* h, void* const* y, float* const* rstd, void* const* y8, int p,
+                                           size_t rows, size_t hidden, size_t group, float eps, coll_dtype_t dtype,
+                                           coll_dtype_t wdtype, void* stream) {
+  return rms_forward(x, residual, gamma, h, y, rstd, y8, true, p, rows, hidden, group, eps, dtype, wdtype, stream);
+}
+
+COLL_EXPORT size_t coll_rmsnorm_workspace_bytes(int p, size_t rows, size_t hidden) {
+  size_t t;
+  if (p < 1 || p > kMaxRanks || hidden == 0 || hidden >= (size_t{1} << 31) || !mul_ok(rows, hidden, 4 * (size_t)kMaxRanks, &t))
+    return 0;
+  return rms_workspace(p, rows, hidden);
+}
+
+COLL_EXPORT coll_status_t coll_rmsnorm_backward(const void* const* dy, const void* const* dh, const void* const* h,
+                                                const float* const* rstd, const void* const* gamma, void* const* dx,
+                                                void* const* dgamma, int p, size_t rows, size_t hidden, coll_op_t op,
+                                                coll_dtype_t dtype, coll_dtype_t wdtype, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+  size_t bytes, unused;
+  coll_status_t st = check_ln_shape(p, rows, hidden, 0, false, dtype, wdtype, &bytes, &unused);
+  if (st != COLL_OK) return st;
+  if (!op_ok(op)) return COLL_ERR_INVALID_ARG;
+  if (op != COLL_SUM && op != COLL_AVG) return COLL_ERR_UNSUPPORTED;
+  const size_t d = dsize(dtype), w = dsize(wdtype);
+  if (!none_or_all(dgamma, p) || !aligned_or_none(dgamma, p, w)) return COLL_ERR_INVALID_ARG;
+  RangeSet rs;
+  rs.add_all(dgamma, p, hidden * w, true);
+  if (rows > 0) {
+    if (!all_non_null(dy, p) || !none_or_all(dh, p) || !all_non_null(h, p) || !all_non_null(rstd, p) ||
+        !all_non_null(dx, p) || !none_or_all(gamma, p))
+      return COLL_ERR_INVALID_ARG;
+    if (!elem_aligned(dy, p, d) || !aligned_or_none(dh, p, d) || !elem_aligned(h, p, d) || !elem_aligned(rstd, p, 4) ||
+        !elem_aligned(dx, p, d) || !aligned_or_none(gamma, p, w))
+      return COLL_ERR_INVALID_ARG;
+    const size_t need = rms_workspace(p, rows, hidden);
+    if (!workspace || !elem_aligned1(workspace, 16) || workspace_bytes < need) return COLL_ERR_INVALID_ARG;
+    rs.add(workspace, need, true);
+    rs.add_in_place(dy, dx, p, bytes);
+    for (int r = 0; dh && r < p; ++r)
+      if (dh[r] != dx[r]) rs.add(dh[r], bytes, false);
+    rs.add_all(h, p, bytes, false);
+    rs.add_all(rstd, p, rows * 4, false);
+    rs.add_all(gamma, p, hidden * w, false);
+  }
+  st = rs.check();
+  if (st != COLL_OK) return st;
+  const uint32_t groups = coll::rms_backward_groups(p, rows, hidden);
+  for (int r0 = 0; rows > 0 && r0 < p; r0 += coll::kArgRanks) {
+    const int n = std::min(p - r0, coll::kArgRanks);
+    coll::RmsArgs a{};
+    for (int r = 0; r < n; ++r) {
+      a.x[r] = dy[r0 + r];
+      if (dh) a.res[r] = dh[r0 + r];
+      a.h[r] = const_cast<void*>(h[r0 + r]);
+      a.rstd[r] = const_cast<float*>(rstd[r0 + r]);
+      if (gamma) a.gamma[r] = gamma[r0 + r];
+      a.y[r] = dx[r0 + r];
+    }
+    a.ws = (float*)workspace + (size_t)(r0 / coll::kArgRanks) * groups * hidden;
+    a.rows = rows;
+    a.hidden = hidden;
+    a.ranks = n;
+    const int e = coll::launch_rms_backward(dtype, wdtype, a, dh != nullptr, groups, stream);
+    if (e) return hip_fail(e);
+  }
+  if (!dgamma) return COLL_OK;
+  coll::LnJoinArgs j{};
+  for (int r = 0; r < p; ++r) j.dgamma[r] = dgamma[r];
+  j.ws = (const float*)workspace;
+  j.hidden = hidden;
+  j.sums = 1;
+  j.parts = rows ? (uint32_t)ln_launches(p) * groups : 0;  // no rows: the sum is zero
+  j.p = p;
+  j.avg = op == COLL_AVG;
+  return finish(coll::launch_ln_join(wdtype, j, stream));
 }
 
 COLL_EXPORT size_t coll_ckpt8_row_bytes(size_t hidden, size_t group) {

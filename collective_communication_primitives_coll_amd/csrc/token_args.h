@@ -37,12 +37,31 @@ struct LnArgs {
 struct LnJoinArgs {
   void* dgamma[kMaxRanks];       // null where absent
   void* dbeta[kMaxRanks];
-  const float* ws;               // [parts][2][hidden]
+  const float* ws;               // [parts][sums][hidden]
   uint64_t hidden;
-  uint64_t first;                // column of this launch's first sum, of 2 * hidden (set by the launcher)
+  uint64_t sums;                 // 2: dgamma's, then dbeta's; 1: dgamma's alone
+  uint64_t first;                // column of this launch's first sum, of sums * hidden (set by the launcher)
   uint32_t parts;
   int p;
   int avg;
+};
+
+// RMS norm, forward and backward.
+struct RmsArgs {
+  const void* x[kArgRanks];      // forward: rows; backward: dy
+  const void* res[kArgRanks];    // the residual; backward: dh (null: none, on every rank)
+  const void* gamma[kArgRanks];  // or null: ones
+  void* h[kArgRanks];            // forward with a residual: written unless null; backward: read
+  float* rstd[kArgRanks];        // forward: written unless null; backward: read
+  void* y[kArgRanks];            // forward: written unless null; backward: dx
+  uint8_t* y8[kArgRanks];        // forward in 8 bits
+  float* ws;                     // backward: partial sums [groups][hidden] of this launch
+  uint64_t rows;                 // per rank
+  uint64_t hidden;
+  uint64_t row_bytes;            // of a row in 8 bits
+  uint32_t glog;                 // log2 of its groups' elements
+  int ranks;                     // of this launch
+  float eps;
 };
 
 // 8-bit checkpoints and the gated activation.
@@ -133,6 +152,12 @@ bool ln_forward_keeps(int dtype, uint64_t hidden, uint64_t group);
 int launch_ln_forward(int dtype, int wdtype, const LnArgs& a, bool ckpt, void* stream);
 int launch_ln_backward(int dtype, int wdtype, const LnArgs& a, uint32_t groups, bool ckpt, void* stream);
 int launch_ln_join(int wdtype, const LnJoinArgs& a, void* stream);
+
+// RMS norm.  rms_backward_groups: as ln_backward_groups.  The weights'
+// gradients are joined by launch_ln_join.
+uint32_t rms_backward_groups(int p, uint64_t rows, uint64_t hidden);
+int launch_rms_forward(int dtype, int wdtype, const RmsArgs& a, bool residual, bool fp8, void* stream);
+int launch_rms_backward(int dtype, int wdtype, const RmsArgs& a, bool dh, uint32_t groups, void* stream);
 
 // 8-bit checkpoints and the gated activation (kind: Ckpt8Kind).
 int launch_ckpt8(int kind, int dtype, Ckpt8Args a, int ranks, void* stream);

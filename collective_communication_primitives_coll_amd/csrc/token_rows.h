@@ -185,9 +185,7 @@ void row_shape(uint64_t hidden, int* tpr, int* nu) {
 
 // Calls f with the shape as compile-time constants.
 template <class F>
-int with_shape(uint64_t hidden, F f) {
-  int tpr, nu;
-  row_shape(hidden, &tpr, &nu);
+int with_shape(int tpr, int nu, F f) {
   const std::integral_constant<int, 1> one;
   const std::integral_constant<int, 2> two;
   if (tpr == 16) return nu == 1 ? f(std::integral_constant<int, 16>(), one) : f(std::integral_constant<int, 16>(), two);
@@ -198,6 +196,13 @@ int with_shape(uint64_t hidden, F f) {
   if (tpr == 512) return f(std::integral_constant<int, 512>(), two);
   if (tpr == 768) return f(std::integral_constant<int, 768>(), two);
   return f(std::integral_constant<int, 1024>(), two);
+}
+
+template <class F>
+int with_shape(uint64_t hidden, F f) {
+  int tpr, nu;
+  row_shape(hidden, &tpr, &nu);
+  return with_shape(tpr, nu, f);
 }
 
 // Workgroups that share a row's columns in the wide backward pass.

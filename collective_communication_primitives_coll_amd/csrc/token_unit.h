@@ -259,12 +259,13 @@ __device__ __forceinline__ float over_448(float a) {
   return __builtin_fmaf(__builtin_fmaf(-q, 448.0f, a), y, q);
 }
 
-// Every lane of the wave calls it (lanes without a unit with zeros).
-template <int DT, int E>
-__device__ __forceinline__ RawUnit<kE4M3, E> encode_unit(const RawUnit<DT, E>& r, const float (&f)[E], uint32_t glog) {
+// The encoding of f, whose largest magnitude in this lane is `mine`.  Every
+// lane of the wave calls it (lanes without a unit with zeros).
+template <int E>
+__device__ __forceinline__ RawUnit<kE4M3, E> encode_amax(uint32_t mine, const float (&f)[E], uint32_t glog) {
 #pragma clang fp contract(off)
   constexpr uint32_t ELOG = E == 8 ? 3 : 2;
-  const uint32_t m = run_max(unit_amax<DT, E>(r), glog - ELOG);
+  const uint32_t m = run_max(mine, glog - ELOG);
   const float amax = fmaxf(__uint_as_float(m), 0x1p-110f);
   const float inv = 448.0f / amax;
   RawUnit<kE4M3, E> q;
@@ -272,6 +273,18 @@ __device__ __forceinline__ RawUnit<kE4M3, E> encode_unit(const RawUnit<DT, E>& r
   for (int h = 0; h < E / 4; ++h) q.c[h] = e4m3_pack(f[4 * h] * inv, f[4 * h + 1] * inv, f[4 * h + 2] * inv, f[4 * h + 3] * inv);
   q.s = m < 0x7f800000u ? over_448(amax) : __uint_as_float(0x7fc00000u);
   return q;
+}
+template <int DT, int E>
+__device__ __forceinline__ RawUnit<kE4M3, E> encode_unit(const RawUnit<DT, E>& r, const float (&f)[E], uint32_t glog) {
+  return encode_amax<E>(unit_amax<DT, E>(r), f, glog);
+}
+// Of values that are in no unit yet.
+template <int E>
+__device__ __forceinline__ RawUnit<kE4M3, E> encode_values(const float (&f)[E], uint32_t glog) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+  return encode_amax<E>(m, f, glog);
 }
 
 // Stores the codes from element `at`, their group's scale (the group's first

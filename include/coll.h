@@ -469,6 +469,57 @@ coll_status_t coll_layernorm_backward(const void* const* dy, const void* const* 
 /* Workspace of the backward pass; 0 if the shape is not accepted. */
 size_t coll_layernorm_workspace_bytes(int p, size_t rows, size_t hidden);
 
+/* RMS norm with the residual's addition before it, forward.  For every row
+ *   h = x + residual  (x without one), in fp32, rounded once to dtype,
+ *   s = 1 / sqrt(mean h^2 + eps),   y = h s gamma.
+ * x[r], residual[r] (optional), h[r] (optional, with a residual only: the
+ * stream that the next layer adds to), y[r]: `rows` rows of `hidden`
+ * elements of dtype.  gamma[r]: rank r's copy of the weights, `hidden`
+ * elements of wdtype (COLL_F32, or dtype); optional (ones).  rstd[r]: fp32
+ * [rows], s for the backward pass; optional.  Statistics are those of the
+ * rounded h, whether it is stored or not, and hold over the whole range of
+ * fp32 values.  A row of zeros with eps = 0 gives NaN.
+ * In place: h[r] and y[r] may each be x[r] or residual[r] (not both the
+ * same).  1 <= hidden < 2^31; rows == 0 is a no-op. */
+coll_status_t coll_rmsnorm(const void* const* x, const void* const* residual, const void* const* gamma,
+                           void* const* h, void* const* y, float* const* rstd, int p, size_t rows, size_t hidden,
+                           float eps, coll_dtype_t dtype, coll_dtype_t wdtype, void* stream);
+
+/* The same with the output in 8 bits, ready to travel (coll_allgather and
+ * the All-to-All forms with COLL_U8): y8[r] gets rows of
+ * coll_ckpt8_row_bytes(hidden, group) bytes, the fp32 values of y in the
+ * format of coll_moe_pack_fp8, which coll_ckpt8_load and
+ * coll_moe_dequant_fp8 read.  y is optional here.  group and y8 as in
+ * coll_ckpt8_save (16-byte aligned; groups that hold a NaN or an infinity
+ * come back as NaN throughout). */
+coll_status_t coll_rmsnorm_fp8(const void* const* x, const void* const* residual, const void* const* gamma,
+                               void* const* h, void* const* y, float* const* rstd, void* const* y8, int p, size_t rows,
+                               size_t hidden, size_t group, float eps, coll_dtype_t dtype, coll_dtype_t wdtype,
+                               void* stream);
+
+/* RMS norm, backward, with data parallelism's AllReduce of the weights'
+ * gradient.  With n = h s and w = dy gamma, per row
+ *   dx = s (w - n mean(w n)) + dh,
+ * the gradient of x and of the residual alike; dh[r] (optional) is the
+ * gradient that reaches h by the stream.  Over all rows of all ranks
+ *   dgamma = sum dy n,
+ * divided by p for COLL_AVG; op is COLL_SUM or COLL_AVG (others
+ * COLL_ERR_UNSUPPORTED).  Every rank gets the total: dgamma[r] holds
+ * `hidden` elements of wdtype; optional.  h (x where there was no residual)
+ * and rstd are those of the forward pass.  workspace: device memory of at
+ * least coll_rmsnorm_workspace_bytes(p, rows, hidden) bytes, 16-byte aligned
+ * (they serve every smaller number of rows too).
+ * In place: dx[r] == dy[r] or dx[r] == dh[r].  rows == 0 writes zeros to
+ * dgamma. */
+coll_status_t coll_rmsnorm_backward(const void* const* dy, const void* const* dh, const void* const* h,
+                                    const float* const* rstd, const void* const* gamma, void* const* dx,
+                                    void* const* dgamma, int p, size_t rows, size_t hidden, coll_op_t op,
+                                    coll_dtype_t dtype, coll_dtype_t wdtype, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/* Workspace of the backward pass; 0 if the shape is not accepted. */
+size_t coll_rmsnorm_workspace_bytes(int p, size_t rows, size_t hidden);
+
 /* Activation checkpoints in 8 bits.  A row of `hidden` elements becomes
  * coll_ckpt8_row_bytes(hidden, group) bytes in the format of
  * coll_moe_pack_fp8: e4m3 codes, one fp32 scale per `group` elements, zero

@@ -32,6 +32,20 @@ def layernorm_backward(dy, x, mean, rstd, gamma):
     return rstd[:, None] * (w - c1 - n * c2), (dy * n).sum(axis=0), dy.sum(axis=0), n
 
 
+def rmsnorm(h, gamma, eps):
+    """h [rows, H] -> y, rstd."""
+    rstd = 1.0 / np.sqrt((h * h).mean(axis=1) + eps)
+    return h * rstd[:, None] * gamma, rstd
+
+
+def rmsnorm_backward(dy, h, rstd, gamma, dh=None):
+    """One rank's rows -> dx, sum dy n, and n (the normalised rows)."""
+    n = h * rstd[:, None]
+    w = dy * gamma
+    dx = rstd[:, None] * (w - n * (w * n).mean(axis=1, keepdims=True))
+    return dx if dh is None else dx + dh, (dy * n).sum(axis=0), n
+
+
 def ckpt8_rows(x32, group):
     """Packed checkpoint rows [rows, row_bytes] of float32 rows (finite)."""
     return np.stack([fp8.encode_row(r, group) for r in np.asarray(x32, dtype=np.float32)])
