@@ -28,6 +28,7 @@ COLL_BATCH_NOALLOC_MAX_BYTES = 4 << 20
 
 COLL_U8 = 3
 COLL_A2A_DIRECT, COLL_A2A_LDS_STAGED = 0, 1
+COLL_DISTILL_RENORM, COLL_DISTILL_TAIL, COLL_DISTILL_MAX_TOP = 0, 1, 128
 COLL_PROBE_NT_LOADS, COLL_PROBE_NT_STORES, COLL_PROBE_CLAIM, COLL_PROBE_DEVICE_STORES = 1, 2, 4, 8
 ELEM_BYTES = {COLL_F32: 4, COLL_BF16: 2, COLL_I32: 4, COLL_U8: 1}
 
@@ -106,6 +107,8 @@ def lib() -> ctypes.CDLL:
         "coll_swiglu_backward_ckpt8": [pp, pp, pp, pp, i32, sz, sz, sz, i32, vp],
         "coll_vocab_logprob": [pp, i64p, i64p, vp, f32, pp, pp, pp, i32, pp, pp, i32, sz, i32, vp, sz, vp],
         "coll_vocab_logprob_backward": [pp, i64p, i64p, vp, f32, vp, vp, vp, vp, pp, i64p, i32, sz, i32, vp],
+        "coll_vocab_distill": [pp, i64p, i64p, vp, vp, i32, i32, f32, pp, pp, i32, sz, i32, vp, sz, vp],
+        "coll_vocab_distill_backward": [pp, i64p, i64p, vp, vp, i32, i32, f32, vp, vp, pp, i64p, i32, sz, i32, vp],
         "coll_stream_probe": [pp, i32, pp, i32, sz, i32, ctypes.c_uint, vp, vp],
     }
     for name, args in sig.items():
@@ -128,6 +131,8 @@ def lib() -> ctypes.CDLL:
     L.coll_ckpt8_row_bytes.restype = sz
     L.coll_vocab_logprob_workspace_bytes.argtypes = [i32, sz, i64p, i32]
     L.coll_vocab_logprob_workspace_bytes.restype = sz
+    L.coll_vocab_distill_workspace_bytes.argtypes = [i32, sz, i64p, i32]
+    L.coll_vocab_distill_workspace_bytes.restype = sz
     L.coll_finalize.argtypes = []
     L.coll_finalize.restype = None
     L.coll_set_grid_limit.argtypes = [ctypes.c_int]
@@ -1036,6 +1041,77 @@ def coll_vocab_logprob_backward(logits, targets, stats, dlogp, dlogits, entropy=
     return _run("coll_vocab_logprob_backward", (z, l, v, _addr(targets), float(inv_temp), _addr(stats), _addr(dlogp),
                                                 opt(entropy), opt(dentropy), dz, dl, p, rows, dt, _stream(stream)),
                 "coll_vocab_logprob_backward", defer, (k0, k1, v, l, dl))
+
+
+def _entries(top_idx, top_logp, rows: int | None, top_k: int | None):
+    """Rows and entries a row of a teacher's list."""
+    import torch
+    if hasattr(top_idx, "dtype") and top_idx.dtype != torch.int32:
+        raise ValueError("top_idx must be a device int32 tensor")
+    _f32("top_logp", [top_logp])
+    if rows is None or top_k is None:
+        if not hasattr(top_idx, "dim") or top_idx.dim() != 2:
+            raise ValueError("rows and top_k must be given unless top_idx is [rows, top_k]")
+        rows = int(top_idx.shape[0]) if rows is None else int(rows)
+        top_k = int(top_idx.shape[1]) if top_k is None else int(top_k)
+    _check_sizes([top_idx, top_logp], int(rows) * int(top_k), "vocab_distill entries")
+    if hasattr(top_idx, "dim") and top_idx.dim() == 2 and rows > 1 and top_idx.shape[1] != top_k:
+        raise ValueError(f"vocab_distill entries: rows of {top_idx.shape[1]}, top_k is {top_k}")
+    if hasattr(top_logp, "dim") and top_logp.dim() == 2 and rows > 1 and top_logp.shape[1] != top_k:
+        raise ValueError(f"vocab_distill entries: rows of {top_logp.shape[1]}, top_k is {top_k}")
+    return int(rows), int(top_k)
+
+
+def coll_vocab_distill_workspace_bytes(rows: int, vocab: Sequence[int], top_k: int) -> int:
+    """Workspace of coll_vocab_distill for up to `rows` rows; vocab lists every
+    rank's shard."""
+    return int(lib().coll_vocab_distill_workspace_bytes(len(vocab), int(rows), _i64_array(vocab), int(top_k)))
+
+
+def coll_vocab_distill(logits, top_idx, top_logp, stats, loss, workspace, kind: int = COLL_DISTILL_TAIL,
+                       inv_temp: float = 1.0, vocab: Sequence[int] | None = None, ld: Sequence[int] | None = None,
+                       rows: int | None = None, top_k: int | None = None, dtype: int | None = None,
+                       workspace_bytes: int | None = None, stream=None, defer: bool = False):
+    """Loss of the shards logits[r] [rows, vocab_r] against a teacher's entries
+    top_idx int32 and top_logp fp32 [rows, top_k]; every rank gets stats fp32
+    [rows, 4] and loss fp32 [rows]."""
+    fname = "coll_vocab_distill"
+    p = len(logits)
+    _same_ranks(p, stats, loss)
+    rows, top_k = _entries(top_idx, top_logp, rows, top_k)
+    dt = _dtype_of(logits[0], dtype)
+    _same_dtype(logits, dt)
+    z, v, l, k0 = _shard_array(logits, rows, vocab, ld, "vocab_distill logits")
+    _check_sizes(stats, 4 * rows, "vocab_distill stats")
+    _check_sizes(loss, rows, "vocab_distill loss")
+    _f32("vocab_distill results", stats, loss)
+    ws, nbytes = _workspace(workspace, workspace_bytes)
+    arrays = [_ptr_array(stats), _ptr_array(loss)]
+    return _run(fname, (z, l, v, _addr(top_idx), _addr(top_logp), top_k, int(kind), float(inv_temp),
+                        *[a for a, _ in arrays], p, rows, dt, ws, nbytes, _stream(stream)), fname, defer,
+                (k0, v, l, *[k for _, k in arrays], workspace))
+
+
+def coll_vocab_distill_backward(logits, top_idx, top_logp, stats, dloss, dlogits, kind: int = COLL_DISTILL_TAIL,
+                                inv_temp: float = 1.0, vocab: Sequence[int] | None = None,
+                                ld: Sequence[int] | None = None, dld: Sequence[int] | None = None,
+                                rows: int | None = None, top_k: int | None = None, dtype: int | None = None,
+                                stream=None, defer: bool = False):
+    """Gradient of the logits from one rank's stats of the forward pass and the
+    gradients of the loss, fp32 [rows]."""
+    fname = "coll_vocab_distill_backward"
+    p = len(logits)
+    _same_ranks(p, dlogits)
+    rows, top_k = _entries(top_idx, top_logp, rows, top_k)
+    dt = _dtype_of(logits[0], dtype)
+    _same_dtype([*logits, *dlogits], dt)
+    z, v, l, k0 = _shard_array(logits, rows, vocab, ld, "vocab_distill_backward logits")
+    dz, dv, dl, k1 = _shard_array(dlogits, rows, list(v), dld, "vocab_distill_backward dlogits")
+    _check_sizes([stats], 4 * rows, "vocab_distill_backward stats")
+    _check_sizes([dloss], rows, "vocab_distill_backward dloss")
+    _f32("vocab_distill_backward stats and gradients", [stats, dloss])
+    return _run(fname, (z, l, v, _addr(top_idx), _addr(top_logp), top_k, int(kind), float(inv_temp), _addr(stats),
+                        _addr(dloss), dz, dl, p, rows, dt, _stream(stream)), fname, defer, (k0, k1, v, l, dl))
 
 
 def coll_status_string(status: int) -> str:

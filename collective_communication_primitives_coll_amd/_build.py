@@ -37,6 +37,7 @@ SOURCES = [
     "rmsnorm_kernels.hip",
     "ckpt8_kernels.hip",
     "logprob_kernels.hip",
+    "distill_kernels.hip",
     "probe_kernels.hip",
     "batch_noalloc.hip",
     "claim_slots.hip",

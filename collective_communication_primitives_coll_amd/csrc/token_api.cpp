@@ -358,6 +358,56 @@ bool logprob_need(int p, size_t rows, const int64_t* vocab, int top_k, size_t* b
   return mul_ok(rows, (size_t)plan.pieces, coll::logprob_piece_bytes(plan, top_k), bytes);
 }
 
+// The same of the distillation's forward pass.
+bool distill_need(int p, size_t rows, const int64_t* vocab, int top_k, size_t* bytes) {
+  coll::LogprobPlan plan;
+  coll::logprob_plan(p, rows, vocab, &plan);
+  return mul_ok(rows, (size_t)plan.pieces * 8 + (size_t)top_k * 4, 1, bytes);
+}
+
+// The most that any number of rows up to this one needs, by need(rows,
+// bytes).  Fewer rows are cut into more pieces, which may take more: it grows
+// with the rows as long as these want one number of pieces, so the last of
+// each such run decides.
+template <class F>
+size_t most_needed(int p, size_t rows, F need) {
+  size_t most;
+  if (!need(rows, &most)) return 0;
+  for (uint64_t want = 2; want <= coll::kMaxPieces; ++want) {
+    const uint64_t last = coll::logprob_most_rows(p, want);
+    size_t bytes;
+    if (last < rows && need((size_t)last, &bytes)) most = std::max(most, bytes);
+  }
+  return most;
+}
+
+// Whether the outputs of the logits' kind, one block a rank, overlap each
+// other, an input of theirs (in place apart) or one of the `n` other ranges.
+bool blocks_alias(const void* const* in, const int64_t* ld, void* const* out, const int64_t* old, const int64_t* vocab, int p,
+                  size_t rows, size_t d, const void* const* small, const size_t* small_bytes, int n) {
+  for (int r = 0; r < p; ++r) {
+    const Block o{(uintptr_t)out[r], rows, (size_t)old[r] * d, (size_t)vocab[r] * d};
+    for (int k = 0; k < n; ++k)
+      if (small[k] && blocks_overlap(o, Block{(uintptr_t)small[k], 1, small_bytes[k], small_bytes[k]})) return true;
+    for (int s = 0; s < p; ++s) {
+      const Block i{(uintptr_t)in[s], rows, (size_t)ld[s] * d, (size_t)vocab[s] * d};
+      const bool in_place = s == r && i.at == o.at && i.stride == o.stride;
+      if (!in_place && blocks_overlap(o, i)) return true;
+      const Block other{(uintptr_t)out[s], rows, (size_t)old[s] * d, (size_t)vocab[s] * d};
+      if (s < r && blocks_overlap(o, other)) return true;
+    }
+  }
+  return false;
+}
+
+// Arguments that both passes of the distillation share.
+coll_status_t check_distill(int p, int top_k, int kind, float inv_temp, int dtype) {
+  if (p < 1 || p > kMaxRanks || top_k < 1 || !(inv_temp > 0.0f) || inv_temp > 1e30f) return COLL_ERR_INVALID_ARG;
+  if (kind != COLL_DISTILL_RENORM && kind != COLL_DISTILL_TAIL) return COLL_ERR_INVALID_ARG;
+  if (top_k > COLL_DISTILL_MAX_TOP) return COLL_ERR_UNSUPPORTED;
+  return float_dtype(dtype);
+}
+
 }  // namespace
 
 COLL_EXPORT coll_status_t coll_layernorm(const void* const* x, const void* const* gamma, const void* const* beta,
@@ -567,17 +617,7 @@ COLL_EXPORT size_t coll_vocab_logprob_workspace_bytes(int p, size_t rows, const 
   if (p < 1 || p > kMaxRanks || !vocab || top_k < 0 || top_k > coll::kMaxTop) return 0;
   for (int r = 0; r < p; ++r)
     if (vocab[r] < 0 || vocab[r] > 0x7fffffffll) return 0;
-  // Fewer rows are cut into more pieces, which may take more: the most that
-  // any number of rows up to this one needs.  It grows with the rows as long
-  // as these want one number of pieces, so the last of each such run decides.
-  size_t most;
-  if (!logprob_need(p, rows, vocab, top_k, &most)) return 0;
-  for (uint64_t want = 2; want <= coll::kMaxPieces; ++want) {
-    const uint64_t last = coll::logprob_most_rows(p, want);
-    size_t bytes;
-    if (last < rows && logprob_need(p, last, vocab, top_k, &bytes)) most = std::max(most, bytes);
-  }
-  return most;
+  return most_needed(p, rows, [&](size_t n, size_t* bytes) { return logprob_need(p, n, vocab, top_k, bytes); });
 }
 
 COLL_EXPORT coll_status_t coll_vocab_logprob(const void* const* logits, const int64_t* ld, const int64_t* vocab,
@@ -657,18 +697,7 @@ COLL_EXPORT coll_status_t coll_vocab_logprob_backward(const void* const* logits,
   if (dentropy && (!entropy || !elem_aligned1(entropy, 4) || !elem_aligned1(dentropy, 4))) return COLL_ERR_INVALID_ARG;
   const void* small[5] = {targets, stats, dlogp, dentropy ? entropy : nullptr, dentropy};
   const size_t small_bytes[5] = {rows * 8, rows * 8, rows * 4, rows * 4, rows * 4};
-  for (int r = 0; r < p; ++r) {
-    const Block out{(uintptr_t)dlogits[r], rows, (size_t)dld[r] * d, (size_t)vocab[r] * d};
-    for (int k = 0; k < 5; ++k)
-      if (small[k] && blocks_overlap(out, Block{(uintptr_t)small[k], 1, small_bytes[k], small_bytes[k]})) return COLL_ERR_ALIAS;
-    for (int s = 0; s < p; ++s) {
-      const Block in{(uintptr_t)logits[s], rows, (size_t)ld[s] * d, (size_t)vocab[s] * d};
-      const bool in_place = s == r && in.at == out.at && in.stride == out.stride;
-      if (!in_place && blocks_overlap(out, in)) return COLL_ERR_ALIAS;
-      const Block other{(uintptr_t)dlogits[s], rows, (size_t)dld[s] * d, (size_t)vocab[s] * d};
-      if (s < r && blocks_overlap(out, other)) return COLL_ERR_ALIAS;
-    }
-  }
+  if (blocks_alias(logits, ld, dlogits, dld, vocab, p, rows, d, small, small_bytes, 5)) return COLL_ERR_ALIAS;
   for (int r = 0; r < p; ++r) {
     a.logits[r] = logits[r];
     a.dlogits[r] = dlogits[r];
@@ -684,4 +713,105 @@ COLL_EXPORT coll_status_t coll_vocab_logprob_backward(const void* const* logits,
   a.scale = inv_temp;
   a.p = p;
   return finish(coll::launch_logprob_backward(dtype, a, stream));
+}
+
+static_assert(COLL_DISTILL_MAX_TOP == coll::kMaxDistill, "entry limit mismatch");
+
+COLL_EXPORT size_t coll_vocab_distill_workspace_bytes(int p, size_t rows, const int64_t* vocab, int top_k) {
+  if (p < 1 || p > kMaxRanks || !vocab || top_k < 1 || top_k > COLL_DISTILL_MAX_TOP) return 0;
+  for (int r = 0; r < p; ++r)
+    if (vocab[r] < 0 || vocab[r] > 0x7fffffffll) return 0;
+  return most_needed(p, rows, [&](size_t n, size_t* bytes) { return distill_need(p, n, vocab, top_k, bytes); });
+}
+
+COLL_EXPORT coll_status_t coll_vocab_distill(const void* const* logits, const int64_t* ld, const int64_t* vocab,
+                                             const int32_t* top_idx, const float* top_logp, int top_k,
+                                             coll_distill_t kind, float inv_temp, float* const* stats,
+                                             float* const* loss, int p, size_t rows, coll_dtype_t dtype,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+  coll_status_t st = check_distill(p, top_k, kind, inv_temp, dtype);
+  if (st != COLL_OK) return st;
+  const size_t d = dsize(dtype);
+  coll::DistillArgs a{};
+  st = check_shards(logits, ld, vocab, p, rows, d, a.first_index);
+  size_t entries;
+  if (st == COLL_OK && !mul_ok(rows, (size_t)top_k, 4, &entries)) st = COLL_ERR_INVALID_ARG;
+  if (st != COLL_OK || rows == 0) return st;
+  if (!top_idx || !top_logp || !elem_aligned1(top_idx, 4) || !elem_aligned1(top_logp, 4) || !all_non_null(stats, p) ||
+      !all_non_null(loss, p) || !elem_aligned(stats, p, 4) || !elem_aligned(loss, p, 4))
+    return COLL_ERR_INVALID_ARG;
+  coll::logprob_plan(p, rows, vocab, &a.plan);
+  size_t need;
+  if (!distill_need(p, rows, vocab, top_k, &need)) return COLL_ERR_INVALID_ARG;
+  if (!workspace || !elem_aligned1(workspace, 16) || workspace_bytes < need) return COLL_ERR_INVALID_ARG;
+  RangeSet rs;
+  for (int r = 0; r < p; ++r) rs.add(logits[r], shard_bytes(rows, ld[r], vocab[r], d), false);
+  rs.add(top_idx, rows * (size_t)top_k * 4, false);
+  rs.add(top_logp, rows * (size_t)top_k * 4, false);
+  rs.add(workspace, need, true);
+  rs.add_all(stats, p, rows * 16, true);
+  rs.add_all(loss, p, rows * 4, true);
+  st = rs.check();
+  if (st != COLL_OK) return st;
+  coll::DistillJoinArgs j{};
+  for (int r = 0; r < p; ++r) {
+    a.logits[r] = logits[r];
+    a.ld[r] = ld[r];
+    j.stats[r] = stats[r];
+    j.loss[r] = loss[r];
+  }
+  a.idx = j.idx = top_idx;
+  a.part = (float*)workspace;
+  a.zs = a.part + rows * (size_t)a.plan.pieces * 2;
+  a.rows = rows;
+  a.scale = j.scale = inv_temp;
+  a.p = j.p = p;
+  a.top = j.top = top_k;
+  j.logp = top_logp;
+  j.part = a.part;
+  j.zs = a.zs;
+  j.rows = rows;
+  j.vocab = a.first_index[p];
+  j.pieces = a.plan.pieces;
+  j.tail = kind == COLL_DISTILL_TAIL;
+  return finish(coll::launch_distill(dtype, a, j, stream));
+}
+
+COLL_EXPORT coll_status_t coll_vocab_distill_backward(const void* const* logits, const int64_t* ld,
+                                                      const int64_t* vocab, const int32_t* top_idx,
+                                                      const float* top_logp, int top_k, coll_distill_t kind,
+                                                      float inv_temp, const float* stats, const float* dloss,
+                                                      void* const* dlogits, const int64_t* dld, int p, size_t rows,
+                                                      coll_dtype_t dtype, void* stream) {
+  coll_status_t st = check_distill(p, top_k, kind, inv_temp, dtype);
+  if (st != COLL_OK) return st;
+  const size_t d = dsize(dtype);
+  coll::DistillGradArgs a{};
+  st = check_shards(logits, ld, vocab, p, rows, d, a.first_index);
+  if (st == COLL_OK) st = check_shards((const void* const*)dlogits, dld, vocab, p, rows, d, a.first_index);
+  size_t entries;
+  if (st == COLL_OK && !mul_ok(rows, (size_t)top_k, 4, &entries)) st = COLL_ERR_INVALID_ARG;
+  if (st != COLL_OK || rows == 0) return st;
+  if (!top_idx || !top_logp || !elem_aligned1(top_idx, 4) || !elem_aligned1(top_logp, 4) || !stats || !elem_aligned1(stats, 4) ||
+      !dloss || !elem_aligned1(dloss, 4))
+    return COLL_ERR_INVALID_ARG;
+  const void* small[4] = {top_idx, top_logp, stats, dloss};
+  const size_t small_bytes[4] = {rows * (size_t)top_k * 4, rows * (size_t)top_k * 4, rows * 16, rows * 4};
+  if (blocks_alias(logits, ld, dlogits, dld, vocab, p, rows, d, small, small_bytes, 4)) return COLL_ERR_ALIAS;
+  for (int r = 0; r < p; ++r) {
+    a.logits[r] = logits[r];
+    a.dlogits[r] = dlogits[r];
+    a.ld[r] = ld[r];
+    a.dld[r] = dld[r];
+  }
+  a.idx = top_idx;
+  a.logp = top_logp;
+  a.stats = stats;
+  a.dloss = dloss;
+  a.rows = rows;
+  a.scale = inv_temp;
+  a.p = p;
+  a.top = top_k;
+  a.tail = kind == COLL_DISTILL_TAIL;
+  return finish(coll::launch_distill_backward(dtype, a, stream));
 }

@@ -145,6 +145,49 @@ struct LogprobGradArgs {
   int p;
 };
 
+// Distillation from a teacher's entries over the same shards and pieces.
+constexpr int kMaxDistill = 128;
+struct DistillArgs {
+  const void* logits[kMaxRanks];
+  int64_t ld[kMaxRanks];         // elements from row to row
+  int64_t first_index[kMaxRanks + 1];  // first vocabulary index of each shard, and the end
+  LogprobPlan plan;
+  const int32_t* idx;            // [rows][top]
+  float* part;                   // [rows][pieces][2]: max and sum, without the entries where there is a tail
+  float* zs;                     // [rows][top]: the entries' logits
+  uint64_t rows, first_row;      // this launch's
+  float scale;                   // inverse temperature
+  int p;
+  int top;
+};
+struct DistillJoinArgs {
+  float* stats[kMaxRanks];       // [rows][4]
+  float* loss[kMaxRanks];
+  const int32_t* idx;
+  const float* logp;             // [rows][top]
+  const float* part;
+  const float* zs;
+  uint64_t rows, first_row;      // this launch's
+  int64_t vocab;
+  float scale;
+  int p, top, pieces;
+  int tail;                      // whether all other entries are one more class
+};
+struct DistillGradArgs {
+  const void* logits[kMaxRanks];
+  void* dlogits[kMaxRanks];
+  int64_t ld[kMaxRanks];
+  int64_t dld[kMaxRanks];
+  int64_t first_index[kMaxRanks + 1];
+  const int32_t* idx;
+  const float* logp;
+  const float* stats;            // [rows][4]
+  const float* dloss;
+  uint64_t rows, first_row;      // this launch's
+  float scale;
+  int p, top, tail;
+};
+
 // Layer norm.  ln_backward_groups: workgroups of each launch of the backward
 // pass (they fix its workspace, so they depend on the shape alone).
 uint32_t ln_backward_groups(int p, uint64_t rows, uint64_t hidden);
@@ -171,5 +214,10 @@ inline size_t logprob_piece_bytes(const LogprobPlan& plan, int top) {
 void logprob_plan(int p, uint64_t rows, const int64_t* vocab, LogprobPlan* plan);
 int launch_logprob(int dtype, const LogprobArgs& a, const LogprobJoinArgs& j, void* stream);
 int launch_logprob_backward(int dtype, const LogprobGradArgs& a, void* stream);
+
+// Distillation: the pieces' pass (a.plan: logprob_plan's) and the join over
+// them, then the logits' gradient.
+int launch_distill(int dtype, const DistillArgs& a, const DistillJoinArgs& j, void* stream);
+int launch_distill_backward(int dtype, const DistillGradArgs& a, void* stream);
 
 }  // namespace coll

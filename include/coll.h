@@ -613,6 +613,64 @@ coll_status_t coll_vocab_logprob_backward(const void* const* logits, const int64
                                           void* const* dlogits, const int64_t* dld, int p, size_t rows,
                                           coll_dtype_t dtype, void* stream);
 
+/* Distillation from a teacher's top entries over a sharded vocabulary: the
+ * divergence of the student's distribution, p_j = softmax(z t)_j over the
+ * shards of coll_vocab_logprob (logits, ld, vocab, inv_temp = t as there),
+ * from the teacher's, of which the `top_k` likeliest entries are known:
+ *   top_idx[row][i], top_logp[row][i]  device int32 and fp32, one copy for
+ *               all ranks: vocabulary index and log probability l_i at the
+ *               loss's temperature, in any order, as coll_vocab_logprob gives
+ *               them.  An index outside the vocabulary is an absent entry; of
+ *               an index listed twice the first entry counts.  1 <= top_k <=
+ *               COLL_DISTILL_MAX_TOP (else COLL_ERR_UNSUPPORTED).
+ * COLL_DISTILL_RENORM: the teacher knows its entries alone (l_i may then be
+ *   logits too, up to a constant of the row): q_i = e^l_i / sum e^l,
+ *     loss = sum q_i (log q_i - log p_i).
+ * COLL_DISTILL_TAIL: all other entries are one more class, in which the
+ *   teacher has q_0 = 1 - sum e^l_i and the student p_0: q_i = e^l_i,
+ *     loss = sum q_i (log q_i - log p_i) + q_0 (log q_0 - log p_0).
+ *   Where all other logits are masked (by -infinity, or by a value so low that
+ *   their sum is below e^-10000 of the largest), q_0 is the rounding of a sum
+ *   that should be 1, and its term is left out.
+ * Terms of q = 0 are 0.  Every rank gets
+ *   loss[r]     fp32 [rows];
+ *   stats[r]    fp32 [rows][4], for the backward pass: m and L as in
+ *               coll_vocab_logprob, then log sum e^l and 0 (RENORM), or the log
+ *               of the sum of e^((z_j - m) t) over the other entries and
+ *               1 - sum e^l_i (TAIL).
+ * A row without entries (RENORM: without any above -infinity) is padding:
+ * loss 0 and, whatever its logits are, no gradient; its last two stats are
+ * +infinity and 0.  Masked logits (-infinity) have p = 0: the loss is
+ * +infinity where the teacher's mass meets none.  A row all masked: m = L =
+ * -inf, loss +infinity, no gradient.  A row that holds a NaN or +infinity
+ * (logits or top_logp): loss and gradient NaN.
+ * workspace: coll_vocab_distill_workspace_bytes(p, rows, vocab, top_k) bytes,
+ * 16-byte aligned; as many serve every smaller number of rows too.
+ * rows == 0 is a no-op. */
+#define COLL_DISTILL_MAX_TOP 128
+typedef enum { COLL_DISTILL_RENORM = 0, COLL_DISTILL_TAIL = 1 } coll_distill_t;
+
+coll_status_t coll_vocab_distill(const void* const* logits, const int64_t* ld, const int64_t* vocab,
+                                 const int32_t* top_idx, const float* top_logp, int top_k, coll_distill_t kind,
+                                 float inv_temp, float* const* stats, float* const* loss, int p, size_t rows,
+                                 coll_dtype_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+size_t coll_vocab_distill_workspace_bytes(int p, size_t rows, const int64_t* vocab, int top_k);
+
+/* The logits' gradient: stats are one rank's results of the forward pass,
+ * dloss fp32 [rows] the gradients of the loss;
+ *   dlogits_j = t dloss (p_j - q_j)              at the teacher's entries,
+ *   dlogits_j = t dloss (p_0 - q_0) p_j / p_0    elsewhere (TAIL),
+ *   dlogits_j = t dloss p_j                      elsewhere (RENORM),
+ * the p's times max(1, sum e^l_i) with TAIL (sum e^l_i where the others are all
+ * masked), written to rank r's shard with
+ * dld[r] elements from row to row.  In place: dlogits[r] == logits[r] with
+ * dld[r] == ld[r]. */
+coll_status_t coll_vocab_distill_backward(const void* const* logits, const int64_t* ld, const int64_t* vocab,
+                                          const int32_t* top_idx, const float* top_logp, int top_k,
+                                          coll_distill_t kind, float inv_temp, const float* stats, const float* dloss,
+                                          void* const* dlogits, const int64_t* dld, int p, size_t rows,
+                                          coll_dtype_t dtype, void* stream);
+
 /* Direction-mix bandwidth probe: a measurement helper, not a collective.
  * [A] 4.1 models a collective's time by the bandwidth of each resource it
  * uses, and [A] 2.5 compares bus bandwidth with what the hardware

@@ -129,3 +129,79 @@ def logprob_backward(z, targets, t, stats, dlogp, entropy, dentropy):
             dz[i, targets[i]] += g
         dz[i] *= t
     return dz
+
+
+def distill(z, idx, logp, t, tail):
+    """z [rows, V] (-inf: masked), the teacher's entries idx and logp [rows, K], t = inverse temperature, tail: all
+    other entries are one more class.  Returns a dict of stats [rows, 4], loss, and, for tolerances, among
+    [rows, V] (which entries are listed), q [rows, V] and d = (z - m) t."""
+    rows, v = z.shape
+    out = {"stats": np.full((rows, 4), np.nan), "loss": np.full(rows, np.nan), "among": np.zeros((rows, v), dtype=bool),
+           "q": np.zeros((rows, v)), "d": np.full((rows, v), np.nan)}
+    for i in range(rows):
+        lq = np.full(v, -np.inf)
+        among = out["among"][i]
+        for j, lj in zip(idx[i], logp[i]):
+            if 0 <= j < v and not among[j]:
+                among[j], lq[j] = True, lj
+        padding = not among.any() if tail else not (among & ~np.isneginf(lq)).any()
+        if padding:
+            out["loss"][i], out["stats"][i, 2:] = 0.0, (np.inf, 0.0)
+        broken = np.isnan(lq).any() or np.isposinf(lq).any()
+        if tail:
+            q, fourth = np.exp(lq), 1.0 - np.exp(lq).sum()
+        elif broken or padding:
+            q, fourth = np.full(v, np.nan), 0.0
+        else:
+            total = np.log(np.exp(lq - lq.max()).sum()) + lq.max()
+            q, fourth = np.exp(lq - total), 0.0
+        if broken:
+            q, fourth = np.full(v, np.nan), np.nan
+        out["q"][i] = q
+        if np.isnan(z[i]).any() or np.isposinf(z[i]).any():
+            continue
+        m = z[i].max()
+        if m == -np.inf:
+            out["stats"][i, :2] = -np.inf
+            if not padding:
+                out["loss"][i] = np.inf
+                out["stats"][i, 2:] = (-np.inf, fourth) if tail else (total if not broken else np.nan, 0.0)
+            continue
+        d = (z[i] - m) * t
+        ls = np.log(np.exp(d).sum())
+        out["stats"][i, :2], out["d"][i] = (m, ls), d
+        if padding:
+            continue
+        rest = d[~among]
+        far = rest.max() if rest.size else -np.inf
+        ltail = np.log(np.exp(rest - far).sum()) + far if far > -np.inf else -np.inf
+        if ltail < -1e4:                                    # masks of a type's lowest value: none are allowed
+            ltail = -np.inf
+        out["stats"][i, 2:] = (ltail, fourth) if tail else (np.nan if broken else total, 0.0)
+        if broken:
+            continue
+        with np.errstate(invalid="ignore"):
+            loss = np.where(q > 0, q * ((lq if tail else lq - total) - (d - ls)), 0.0).sum()
+        if tail and fourth > 0 and ltail > -np.inf:  # (left out where no other entry is allowed)
+            loss += fourth * (np.log(fourth) - (ltail - ls))
+        out["loss"][i] = loss
+    return out
+
+
+def distill_backward(z, among, q, t, stats, dloss, tail):
+    """dz [rows, V] from the forward pass's stats; among and q as distill gives them."""
+    dz = np.zeros(z.shape)
+    for i in range(len(z)):
+        m, ls, third, fourth = stats[i]
+        if third == np.inf or m == -np.inf:
+            continue
+        d = (z[i] - m) * t
+        p = np.exp(d - ls)
+        if tail:
+            rest, whole = (fourth if not fourth <= 0 else 0.0), (1.0 - fourth if not fourth >= 0 or third == -np.inf else 1.0)
+            others = 0.0 * p if third == -np.inf else np.exp(d - third) * (whole * np.exp(third - ls) - rest)
+            dz[i] = np.where(among[i], whole * p - q[i], others)
+        else:
+            dz[i] = np.where(among[i], p - q[i], p + (third - third))
+        dz[i] *= dloss[i] * t
+    return dz
