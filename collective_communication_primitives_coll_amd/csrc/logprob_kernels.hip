@@ -142,6 +142,9 @@ struct Running {
   }
   __device__ __forceinline__ void wave_join(float c) {
     rebase(wave_max(m), c);
+    // The products are rounded here: fused with one addend of the sums, they
+    // would make these sums other ones on every lane, and so on every rank.
+    asm volatile("" : "+v"(s), "+v"(a));
     s = wave_sum(s);
     a = wave_sum(a);
   }
