@@ -53,6 +53,24 @@ class coll_call_t(ctypes.Structure):
     ]
 
 
+class coll_adjust_t(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_void_p),
+        ("ntokens", ctypes.c_size_t),
+        ("offsets", ctypes.c_void_p),
+        ("prompt", ctypes.c_void_p),
+        ("repetition", ctypes.c_void_p),
+        ("presence", ctypes.c_void_p),
+        ("frequency", ctypes.c_void_p),
+        ("bias_idx", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("nbias", ctypes.c_size_t),
+        ("bias_offsets", ctypes.c_void_p),
+        ("mask", ctypes.c_void_p),
+        ("mask_ld", ctypes.c_int64),
+    ]
+
+
 def lib() -> ctypes.CDLL:
     """Load libcoll.so (raises if it has not been built)."""
     global _lib
@@ -109,6 +127,7 @@ def lib() -> ctypes.CDLL:
         "coll_vocab_logprob_backward": [pp, i64p, i64p, vp, f32, vp, vp, vp, vp, pp, i64p, i32, sz, i32, vp],
         "coll_vocab_distill": [pp, i64p, i64p, vp, vp, i32, i32, f32, pp, pp, i32, sz, i32, vp, sz, vp],
         "coll_vocab_distill_backward": [pp, i64p, i64p, vp, vp, i32, i32, f32, vp, vp, pp, i64p, i32, sz, i32, vp],
+        "coll_vocab_adjust": [pp, i64p, i64p, ctypes.POINTER(coll_adjust_t), pp, i64p, i32, sz, i32, vp],
         "coll_stream_probe": [pp, i32, pp, i32, sz, i32, ctypes.c_uint, vp, vp],
     }
     for name, args in sig.items():
@@ -1112,6 +1131,73 @@ def coll_vocab_distill_backward(logits, top_idx, top_logp, stats, dloss, dlogits
     _f32("vocab_distill_backward stats and gradients", [stats, dloss])
     return _run(fname, (z, l, v, _addr(top_idx), _addr(top_logp), top_k, int(kind), float(inv_temp), _addr(stats),
                         _addr(dloss), dz, dl, p, rows, dt, _stream(stream)), fname, defer, (k0, k1, v, l, dl))
+
+
+def coll_vocab_adjust(logits, out, tokens=None, offsets=None, prompt=None, repetition=None, presence=None,
+                      frequency=None, bias_idx=None, bias=None, bias_offsets=None, mask=None,
+                      ntokens: int | None = None, nbias: int | None = None, mask_ld: int | None = None,
+                      vocab: Sequence[int] | None = None, ld: Sequence[int] | None = None,
+                      old: Sequence[int] | None = None, rows: int | None = None, dtype: int | None = None, stream=None,
+                      defer: bool = False):
+    """Penalties, biases and masks on the shards logits[r] [rows, vocab_r],
+    written to out[r] (the same tensors: in place).  tokens int64 with offsets
+    int64 [rows + 1] and (or None) prompt int64 [rows]: the rows' histories;
+    repetition, presence and frequency (or None) fp32 [rows]; bias_idx int64 and
+    bias fp32 with bias_offsets int64 [rows + 1]; mask int32 or uint32
+    [rows, words], bit j % 32 of word j // 32 for entry j, 1: allowed."""
+    import torch
+    fname = "coll_vocab_adjust"
+    p = len(logits)
+    _same_ranks(p, out)
+    if rows is None:
+        if not hasattr(logits[0], "dim"):
+            raise ValueError("rows must be given for raw addresses")
+        rows = int(logits[0].shape[0])
+    rows = int(rows)
+    dt = _dtype_of(logits[0], dtype)
+    _same_dtype([*logits, *out], dt)
+    z, v, l, k0 = _shard_array(logits, rows, vocab, ld, "vocab_adjust logits")
+    o, _, ol, k1 = _shard_array(out, rows, list(v), old, "vocab_adjust out")
+
+    def buffer(what, x, dtypes, need):
+        if x is None:
+            return None
+        if hasattr(x, "dtype") and x.dtype not in dtypes:
+            raise ValueError(f"vocab_adjust {what}: {x.dtype}")
+        _check_sizes([x], need, f"vocab_adjust {what}")
+        return _addr(x)
+
+    def count(what, x, n):
+        if x is None:
+            if n:
+                raise ValueError(f"vocab_adjust {what} must be given")
+            return 0
+        return _numel(x, n)
+    i64, f32 = (torch.int64,), (torch.float32,)
+    by = coll_adjust_t()
+    by.ntokens, by.nbias = count("tokens", tokens, ntokens), count("bias", bias, nbias)
+    by.tokens, by.offsets = buffer("tokens", tokens, i64, by.ntokens), buffer("offsets", offsets, i64, rows + 1)
+    by.prompt = buffer("prompt", prompt, i64, rows)
+    by.repetition, by.presence = buffer("repetition", repetition, f32, rows), buffer("presence", presence, f32, rows)
+    by.frequency = buffer("frequency", frequency, f32, rows)
+    by.bias_idx, by.bias = buffer("bias_idx", bias_idx, i64, by.nbias), buffer("bias", bias, f32, by.nbias)
+    by.bias_offsets = buffer("bias_offsets", bias_offsets, i64, rows + 1)
+    if mask is not None:
+        words = (sum(v) + 31) // 32
+        if isinstance(mask, int):
+            if mask_ld is None:
+                raise ValueError("mask_ld must be given for raw addresses")
+            by.mask, by.mask_ld = mask, int(mask_ld)
+        else:
+            if mask.dtype not in (torch.int32, torch.uint32) or not mask.is_cuda:
+                raise ValueError("vocab_adjust mask must be a device int32 or uint32 tensor")
+            if mask.dim() != 2 or mask.shape[0] < rows or mask.shape[1] < words or (mask.shape[1] > 1 and mask.stride(1) != 1):
+                raise ValueError(f"vocab_adjust mask: [rows, words] of at least {words} words with contiguous rows")
+            stride = max(int(mask.stride(0)), words) if mask.shape[0] <= 1 else int(mask.stride(0))
+            if mask_ld is not None and mask.shape[0] > 1 and int(mask_ld) != stride:
+                raise ValueError(f"vocab_adjust mask: rows {stride} words apart, mask_ld is {int(mask_ld)}")
+            by.mask, by.mask_ld = mask.data_ptr(), stride
+    return _run(fname, (z, l, v, ctypes.byref(by), o, ol, p, rows, dt, _stream(stream)), fname, defer, (k0, k1, v, l, ol, by))
 
 
 def coll_status_string(status: int) -> str:

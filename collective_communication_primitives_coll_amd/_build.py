@@ -38,6 +38,7 @@ SOURCES = [
     "ckpt8_kernels.hip",
     "logprob_kernels.hip",
     "distill_kernels.hip",
+    "adjust_kernels.hip",
     "probe_kernels.hip",
     "batch_noalloc.hip",
     "claim_slots.hip",

@@ -815,3 +815,56 @@ COLL_EXPORT coll_status_t coll_vocab_distill_backward(const void* const* logits,
   a.tail = kind == COLL_DISTILL_TAIL;
   return finish(coll::launch_distill_backward(dtype, a, stream));
 }
+
+COLL_EXPORT coll_status_t coll_vocab_adjust(const void* const* logits, const int64_t* ld, const int64_t* vocab,
+                                            const coll_adjust_t* by, void* const* out, const int64_t* old, int p,
+                                            size_t rows, coll_dtype_t dtype, void* stream) {
+  if (p < 1 || p > kMaxRanks || !by) return COLL_ERR_INVALID_ARG;
+  coll_status_t st = float_dtype(dtype);
+  if (st != COLL_OK) return st;
+  const size_t d = dsize(dtype);
+  coll::AdjustArgs a{};
+  st = check_shards(logits, ld, vocab, p, rows, d, a.first_index);
+  if (st == COLL_OK) st = check_shards((const void* const*)out, old, vocab, p, rows, d, a.first_index);
+  if (st != COLL_OK) return st;
+  if (by->ntokens > 0x7fffffffu || by->nbias > 0x7fffffffu) return COLL_ERR_UNSUPPORTED;
+  const int64_t words = (a.first_index[p] + 31) / 32;
+  size_t mask_bytes = 0;
+  if (by->mask && (by->mask_ld < words || !mul_ok((size_t)by->mask_ld, rows, 4, &mask_bytes))) return COLL_ERR_INVALID_ARG;
+  if (rows == 0) return COLL_OK;
+  // what counts tokens comes with a history, what adds biases with a list
+  const bool history = by->offsets != nullptr, biases = by->bias_offsets != nullptr;
+  if (!history && (by->tokens || by->ntokens || by->prompt || by->repetition || by->presence || by->frequency)) return COLL_ERR_INVALID_ARG;
+  if (!biases && (by->bias_idx || by->bias || by->nbias)) return COLL_ERR_INVALID_ARG;
+  if ((by->ntokens && !by->tokens) || (by->nbias && (!by->bias_idx || !by->bias))) return COLL_ERR_INVALID_ARG;
+  const void* small[10] = {by->tokens, by->offsets, by->prompt, by->repetition, by->presence,
+                           by->frequency, by->bias_idx, by->bias, by->bias_offsets, by->mask};
+  const size_t align[10] = {8, 8, 8, 4, 4, 4, 8, 4, 8, 4};
+  const size_t small_bytes[10] = {by->ntokens * 8, rows * 8 + 8, rows * 8, rows * 4, rows * 4, rows * 4, by->nbias * 8, by->nbias * 4,
+                                  rows * 8 + 8, by->mask ? ((rows - 1) * (size_t)by->mask_ld + (size_t)words) * 4 : 0};
+  for (int k = 0; k < 10; ++k)
+    if ((uintptr_t)small[k] % align[k]) return COLL_ERR_INVALID_ARG;
+  if (blocks_alias(logits, ld, out, old, vocab, p, rows, d, small, small_bytes, 10)) return COLL_ERR_ALIAS;
+  for (int r = 0; r < p; ++r) {
+    a.logits[r] = logits[r];
+    a.out[r] = out[r];
+    a.ld[r] = ld[r];
+    a.old[r] = old[r];
+  }
+  a.tokens = by->tokens;
+  a.offsets = by->offsets;
+  a.prompt = by->prompt;
+  a.repetition = by->repetition;
+  a.presence = by->presence;
+  a.frequency = by->frequency;
+  a.bias_idx = by->bias_idx;
+  a.bias = by->bias;
+  a.bias_offsets = by->bias_offsets;
+  a.mask = by->mask;
+  a.mask_ld = by->mask_ld;
+  a.ntokens = by->ntokens;
+  a.nbias = by->nbias;
+  a.rows = rows;
+  a.p = p;
+  return finish(coll::launch_adjust(dtype, a, stream));
+}

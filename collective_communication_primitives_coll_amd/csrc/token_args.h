@@ -188,6 +188,32 @@ struct DistillGradArgs {
   int p, top, tail;
 };
 
+// Penalties, biases and masks on the same shards; null where absent.
+struct AdjustArgs {
+  const void* logits[kMaxRanks];
+  void* out[kMaxRanks];
+  int64_t ld[kMaxRanks];         // elements from row to row
+  int64_t old[kMaxRanks];
+  int64_t first_index[kMaxRanks + 1];  // first vocabulary index of each shard, and the end
+  int first[kMaxRanks + 1];      // first run of each shard's rows, and the end (set by the launcher)
+  int chunks;                    // runs of a row
+  uint64_t ranks_q32;            // ranks to a run on average, times 2^32
+  const int64_t* tokens;         // [ntokens], row r's from offsets[r] to offsets[r + 1]
+  const int64_t* offsets;
+  const int64_t* prompt;
+  const float* repetition;       // [rows]
+  const float* presence;
+  const float* frequency;
+  const int64_t* bias_idx;       // [nbias], row r's from bias_offsets[r] to bias_offsets[r + 1]
+  const float* bias;
+  const int64_t* bias_offsets;
+  const uint32_t* mask;          // [rows], mask_ld words apart
+  int64_t mask_ld;
+  uint64_t ntokens, nbias;
+  uint64_t rows, first_row;      // this launch's
+  int p;
+};
+
 // Layer norm.  ln_backward_groups: workgroups of each launch of the backward
 // pass (they fix its workspace, so they depend on the shape alone).
 uint32_t ln_backward_groups(int p, uint64_t rows, uint64_t hidden);
@@ -219,5 +245,7 @@ int launch_logprob_backward(int dtype, const LogprobGradArgs& a, void* stream);
 // them, then the logits' gradient.
 int launch_distill(int dtype, const DistillArgs& a, const DistillJoinArgs& j, void* stream);
 int launch_distill_backward(int dtype, const DistillGradArgs& a, void* stream);
+
+int launch_adjust(int dtype, const AdjustArgs& a, void* stream);
 
 }  // namespace coll

@@ -613,6 +613,53 @@ coll_status_t coll_vocab_logprob_backward(const void* const* logits, const int64
                                           void* const* dlogits, const int64_t* dld, int p, size_t rows,
                                           coll_dtype_t dtype, void* stream);
 
+/* Penalties for repeated tokens, biases and masks on logits over a sharded
+ * vocabulary (logits, ld, vocab as in coll_vocab_logprob), before a token is
+ * chosen from them.  All that `by` points to is device memory, one copy for
+ * all ranks, and optional (NULL):
+ *   tokens, ntokens, offsets   int64: row r's history is tokens[offsets[r]] up
+ *               to tokens[offsets[r + 1]] (rows + 1 offsets, rising, at most
+ *               ntokens < 2^31; what lies outside is not read).  Its first
+ *               prompt[r] tokens (int64 [rows]; 0 without) are the prompt's,
+ *               the others the answer's.  A token outside the vocabulary is
+ *               padding.
+ *   repetition, presence, frequency   fp32 [rows]: with c_j the number of
+ *               times that token j is among the answer's,
+ *                 z_j > 0 ? z_j / repetition : z_j repetition   where the
+ *                                                history has token j,
+ *                 z_j - (c_j frequency + presence)   where c_j > 0;
+ *   bias_idx, bias, nbias, bias_offsets   int64, fp32, and offsets as above
+ *               (nbias < 2^31): added to the entries that row r's part lists.
+ *               Of an index listed twice the first entry counts; one outside
+ *               the vocabulary is padding.
+ *   mask        32-bit words, mask_ld of them from row to row, at least one for
+ *               every 32 entries of the vocabulary: entry j stays where bit
+ *               j % 32 of word j / 32 is 1, and becomes -infinity (a NaN too)
+ *               where it is 0.
+ * In this order, in fp32, rounded once to out[r], whose rows are old[r]
+ * elements apart.  In place: out[r] == logits[r] with old[r] == ld[r].  A
+ * penalty without offsets, or a bias without bias_offsets, is
+ * COLL_ERR_INVALID_ARG.  rows == 0 is a no-op. */
+typedef struct {
+  const int64_t* tokens;
+  size_t ntokens;
+  const int64_t* offsets;
+  const int64_t* prompt;
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const int64_t* bias_idx;
+  const float* bias;
+  size_t nbias;
+  const int64_t* bias_offsets;
+  const uint32_t* mask;
+  int64_t mask_ld;
+} coll_adjust_t;
+
+coll_status_t coll_vocab_adjust(const void* const* logits, const int64_t* ld, const int64_t* vocab,
+                                const coll_adjust_t* by, void* const* out, const int64_t* old, int p, size_t rows,
+                                coll_dtype_t dtype, void* stream);
+
 /* Distillation from a teacher's top entries over a sharded vocabulary: the
  * divergence of the student's distribution, p_j = softmax(z t)_j over the
  * shards of coll_vocab_logprob (logits, ld, vocab, inv_temp = t as there),

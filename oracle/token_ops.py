@@ -205,3 +205,33 @@ def distill_backward(z, among, q, t, stats, dloss, tail):
             dz[i] = np.where(among[i], p - q[i], p + (third - third))
         dz[i] *= dloss[i] * t
     return dz
+
+
+def adjust(z, history=None, prompt=None, repetition=None, presence=None, frequency=None, biases=None, allow=None):
+    """z [rows, V]; history[i]: row i's tokens, the first prompt[i] of them the prompt's; biases[i]: pairs (entry,
+    value); allow [rows, V] truth values.  Returns the adjusted logits and the size of the terms in each."""
+    out = np.array(z, dtype=np.float64)
+    rows, v = out.shape
+    size = np.zeros((rows, v))
+    for i in range(rows):
+        h = np.asarray(history[i] if history else [], dtype=np.int64)
+        inside = lambda t: t[(t >= 0) & (t < v)]  # noqa: E731
+        start = min(max(int(prompt[i]), 0), len(h)) if prompt is not None else 0
+        seen = np.unique(inside(h))
+        count = np.bincount(inside(h[start:]), minlength=v)
+        if repetition is not None:
+            r = float(repetition[i])
+            out[i, seen] = np.where(out[i, seen] > 0, out[i, seen] / r, out[i, seen] * r)
+        size[i] = np.abs(np.where(np.isfinite(out[i]), out[i], 0.0))
+        less = (count * float(frequency[i]) if frequency is not None else 0.0) + (float(presence[i]) if presence is not None else 0.0)
+        out[i] -= np.where(count > 0, less, 0.0)
+        size[i] += 2 * np.abs(np.where(count > 0, less, 0.0))
+        had = set()
+        for j, b in biases[i] if biases else []:
+            if 0 <= j < v and j not in had:
+                had.add(j)
+                out[i, j] += b
+                size[i, j] += abs(b) if np.isfinite(b) else 0.0
+    if allow is not None:
+        out[~allow] = -np.inf
+    return out, size

@@ -102,3 +102,15 @@ def test_distillation_edge_rows():
             assert np.allclose(r["loss"][4], -np.log(p[3])) and r["loss"][5] == 0 and r["stats"][5, 2] == np.inf
         dz = token_ops.distill_backward(z, r["among"], r["q"], 1.0, r["stats"], np.ones(6), tail)
         assert (dz[:3] == 0).all() and np.isfinite(dz).all()
+
+
+def test_adjustment_by_hand():
+    z = np.array([[2.0, -2.0, 0.0, 4.0, -1.0], [1.0, 1.0, 1.0, np.nan, -np.inf]])
+    out, _ = token_ops.adjust(z, [[0, 1, 0, 3, 3, 9, -1], [4]], [2, 0], [2.0, 3.0], [0.5, 0.25], [0.125, 0.0],
+                              [[(4, 10.0), (4, 20.0), (7, 1.0), (0, -np.inf)], []], np.array([[1, 1, 1, 1, 1], [1, 1, 0, 0, 1]], dtype=bool))
+    # row 0: 0 and 1 are the prompt's, then 0 once and 3 twice
+    assert np.array_equal(out[0], [-np.inf, -4.0, 0.0, 2.0 - 0.5 - 0.25, 9.0])
+    assert np.array_equal(out[1], [1.0, 1.0, -np.inf, -np.inf, -np.inf])
+    out, _ = token_ops.adjust(z[:1], [[3, 3, 0]], None, None, None, [1.0])
+    assert np.array_equal(out[0], [1.0, -2.0, 0.0, 2.0, -1.0])
+    assert np.array_equal(token_ops.adjust(z[:1])[0], z[:1])
