@@ -1,29 +1,41 @@
 // Penalties for repeated tokens, biases and masks on logits that lie in p
 // shards.  Per row, with c_j how often token j is among the answer's tokens:
-//   v = z > 0 ? z / repetition : z repetition   where the history has token j,
+//   v = z > 0 ? z (1 / repetition) : z repetition   where the history has token j,
 //   v -= c_j frequency + presence               where c_j > 0,
 //   v += bias                                   where a bias lists entry j,
 //   v = -inf                                    where the mask's bit j is 0
 // in fp32, rounded once.
 //
 // Bound by reading and writing the logits.  A workgroup takes a run of a
-// row's shard.  It asks for the run's logits, counts the row's history in a
-// table of its entries in LDS while they come (every workgroup of a row goes
-// over the whole history, which comes from L2, and keeps what falls into its
-// run), and then goes once over the run.  Counts are whole numbers and a
-// bias's first entry wins by its place in the list, so results do not depend
-// on the order of the atomics.
+// row's shard.  It asks for the run's logits, which stay in registers, and
+// marks the row's history and biases in a table of the run's entries in LDS
+// while they come.  Every workgroup of a row goes over the whole history and
+// keeps what falls into its run: the longer the run the less often, so runs
+// are as long as two workgroups' tables to a CU allow, and a row's runs follow
+// each other on one XCD, whose L2 then serves the history to all but the
+// first.  Few units have a mark: a wave collects its own from its lanes and
+// adjusts them at once, before the mask, which needs no arithmetic.
+// 512 x 131072 bf16 in 8 shards, masks, 100 biases and histories of 4000
+// tokens on average (most shorter, some of 30000 and more): 72 us; 67 with
+// 4000 in every row, 59 without masks and biases, 48 with nothing to mark
+// (5.6 TB/s).  Runs of 8192 entries took 73 for 67, and 82 where a row's runs
+// went to all XCDs; every lane adjusting its own units 85.  Where few rows
+// leave CUs without work, runs are short: 4 rows of 131072, 400 tokens: 5.4 us.
+//
+// Counts are whole numbers and a bias's first entry wins by its place in the
+// list, so results do not depend on the order of the atomics.
 #include "vocab_pieces.h"
 
 namespace coll {
 
 namespace {
 
-// A table word of an entry: its count among the answer's tokens (bits 0..14),
-// whether the prompt has it (bit 15), and kBiasPlaces less the place of its
-// bias in the row's list (bits 16..31; 0: none).  Longer histories and lists
-// take two words an entry, and the run in two halves.
-constexpr uint32_t kPrompt = 0x8000u, kCountMost = 0x7fffu, kBiasPlaces = 0xffffu;
+// A table word of an entry: its count among the answer's tokens (bits 0..19),
+// whether the prompt has it (bit 20), and kBiasMost less the place of its bias
+// in the row's list (bits 21..31; 0: none).  Longer histories and lists take
+// two words an entry, and the run in two halves.
+constexpr uint32_t kCountMost = (1u << 20) - 1, kPrompt = 1u << 20, kSeen = kPrompt | kCountMost, kBiasMost = 2047;
+constexpr int kBiasShift = 21;
 constexpr uint32_t kLongPrompt = 0x80000000u;
 
 // A row's part of a list, as offsets within it that are in bounds whatever
@@ -40,13 +52,23 @@ struct Span {
   }
 };
 
-template <int DT, int UNITS>
-__global__ __launch_bounds__(kBlock) void adjust_kernel(AdjustArgs a) {
+// Tokens that a lane asks for at a time; the next ones while it looks at these.
+constexpr int kTokensAhead = 8;
+
+template <int DT, int THREADS, int UNITS>
+__global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
   constexpr int B = Traits<DT>::B, E = kElems<DT>;
-  constexpr uint32_t kRun = UNITS * kBlock * E;
+  constexpr uint32_t kRun = UNITS * THREADS * E;
+  using S = typename Traits<DT>::S;
   __shared__ __attribute__((aligned(16))) uint32_t table[kRun];
-  const uint32_t in = blockIdx.x / (uint32_t)a.chunks, chunk = blockIdx.x - in * (uint32_t)a.chunks;
-  const uint64_t row = a.first_row + in;
+  __shared__ u32x4 held[THREADS];           // a wave's units to adjust
+  __shared__ uint16_t held_unit[THREADS];
+  __shared__ float first_values[THREADS];   // of the biases, those of the list's first places
+  const uint32_t lane = threadIdx.x, turn = blockIdx.x / (uint32_t)a.spread, group = turn / (uint32_t)a.chunks;
+  const uint32_t chunk = turn - group * (uint32_t)a.chunks;
+  const uint32_t in_row = group * (uint32_t)a.spread + (blockIdx.x - turn * (uint32_t)a.spread);
+  if (in_row >= a.rows) return;
+  const uint64_t row = a.first_row + in_row;
   int r = min((int)((2 * (uint64_t)chunk + 1) * a.ranks_q32 >> 33), a.p - 1);
   while (a.first[r] > (int)chunk) --r;
   while (a.first[r + 1] <= (int)chunk) ++r;
@@ -55,154 +77,271 @@ __global__ __launch_bounds__(kBlock) void adjust_kernel(AdjustArgs a) {
   const int64_t first = a.first_index[r] + at;  // vocabulary index of the run's first entry
   const uint8_t* src = as_global(static_cast<const uint8_t*>(a.logits[r])) + ((int64_t)row * a.ld[r] + at) * B;
   uint8_t* dst = as_global(static_cast<uint8_t*>(a.out[r])) + ((int64_t)row * a.old[r] + at) * B;
+  const Span hist(a.offsets, row, a.ntokens), bias(a.bias_offsets, row, a.nbias);
   const RowBuffer from(src, full * 16), to(dst, full * 16);
   RawUnit<DT, E> z[UNITS];
 #pragma unroll
-  for (int i = 0; i < UNITS; ++i) z[i] = load_unit<DT, E, true>(from, (i * kBlock + threadIdx.x) * E);
-  RawUnit<DT, E> last = zero_unit<DT, E>();
-  const bool ends = part && full % kBlock == threadIdx.x;  // this lane has the run's last elements
-  if (ends) last = load_part<DT, E>(src, full * E, part);
+  for (int i = 0; i < UNITS; ++i) z[i] = load_unit<DT, E, true>(from, (i * THREADS + lane) * E);
+  // the elements behind the last unit, one to a lane (the others load the
+  // run's first, so that nothing waits here)
+  const uint32_t end = lane < part ? full * E + lane : 0;
+  S end_raw = reinterpret_cast<const S*>(src)[end];
+  // The mask's bits of `n` entries from entry `entry` of the run on, as loaded.
+  const uint64_t mask_last = (uint64_t)(a.first_index[a.p] - 1) / 32;
+  const uint32_t* words = as_global(a.mask) + row * (uint64_t)a.mask_ld;
+  auto mask_words = [&](uint32_t entry, uint32_t n, uint32_t (&w)[2]) __attribute__((always_inline)) {
+    const uint64_t bit = (uint64_t)first + entry;
+    // (past the vocabulary: its last word, whose bits are not looked at)
+    w[0] = words[min(bit / 32, mask_last)];
+    w[1] = words[min((bit + n - 1) / 32, mask_last)];
+  };
+  auto mask_bits = [&](uint32_t entry, const uint32_t (&w)[2]) {
+    return (uint32_t)((((uint64_t)w[1] << 32) | w[0]) >> (((uint32_t)first + entry) % 32));
+  };
+  uint32_t mw[UNITS][2], end_mw[2] = {~0u, ~0u};
+  if (a.mask) {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) mask_words((i * THREADS + lane) * E, E, mw[i]);
+    mask_words(end, 1, end_mw);
+  } else {
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) mw[i][0] = mw[i][1] = ~0u;
+  }
 
-  const Span hist(a.offsets, row, a.ntokens), bias(a.bias_offsets, row, a.nbias);
   const int64_t prompt = a.prompt ? ld_const(a.prompt + row) : 0;
   const uint32_t answer = prompt < 0 ? 0 : (uint32_t)min(prompt, (int64_t)hist.n);  // where the answer starts
   const int64_t* tokens = as_global(a.tokens) + hist.begin;
   const int64_t* places = as_global(a.bias_idx) + bias.begin;
   const float* values = as_global(a.bias) + bias.begin;
-  const float repetition = a.repetition ? ld_const(a.repetition + row) : 1.0f;
+  const float repetition = a.repetition ? ld_const(a.repetition + row) : 1.0f, inverse = 1.0f / repetition;
   const float presence = a.presence ? ld_const(a.presence + row) : 0.0f;
   const float frequency = a.frequency ? ld_const(a.frequency + row) : 0.0f;
 
   auto penalize = [&](float v, bool seen, uint32_t count) {
-    if (seen) v = v > 0.0f ? v / repetition : v * repetition;
-    if (count) v -= (float)count * frequency + presence;
+    v *= !seen ? 1.0f : v > 0.0f ? inverse : repetition;
+    return v - (count ? (float)count * frequency + presence : 0.0f);
+  };
+  auto value_at = [&](uint32_t i) { return i < THREADS ? first_values[i] : values[i]; };
+  auto adjust = [&](float v, uint32_t w) {
+    v = penalize(v, w & kSeen, w & kCountMost);
+    if (w >> kBiasShift) v += value_at(kBiasMost - (w >> kBiasShift));
     return v;
   };
-  // the mask's bits of unit u
-  auto mask_out = [&](uint32_t u, float (&f)[E]) {
-    if (!a.mask) return;
-    const uint64_t bit = (uint64_t)first + (uint64_t)u * E;
-    const uint32_t* words = as_global(a.mask) + row * (uint64_t)a.mask_ld;
-    // (where both words are the row's last one, the bits past it are not looked at)
-    const uint64_t w0 = bit / 32, w1 = min((bit + E - 1) / 32, (uint64_t)(a.first_index[a.p] - 1) / 32);
-    const uint32_t allow = (uint32_t)((((uint64_t)words[w1] << 32) | words[w0]) >> (bit % 32));
+  // a unit, by its entries' words
+  auto adjust_unit = [&](const RawUnit<DT, E>& raw, uint32_t u) __attribute__((always_inline)) {
+    uint32_t w[E], any = 0;
+    float f[E];
+    widen_unit(raw, f);
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (!(allow >> e & 1)) f[e] = -__builtin_inff();
+    for (int e = 0; e < E; ++e) any |= w[e] = table[u * E + e];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = penalize(f[e], w[e] & kSeen, w[e] & kCountMost);
+    if (any >> kBiasShift) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (w[e] >> kBiasShift) f[e] += value_at(kBiasMost - (w[e] >> kBiasShift));
+    }
+    return narrow_unit<DT, E>(f);
   };
-  // every unit of the run that `mine` takes, marked by mark(unit, values)
-  auto finish = [&](auto mine, auto mark) {
+  // A list of n places in the vocabulary, from place i0 on, a lane's in t; and
+  // those of them in this run (of `most` entries from vocabulary index `begin`
+  // on): f(entry's place in the run, place in the list).
+  auto ask = [&](auto& t, const int64_t* all, uint32_t n, uint32_t i0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < (int)(sizeof(t) / 8); ++k)
+      if (i0 + k * THREADS < n) t[k] = (uint64_t)all[min(i0 + k * THREADS + lane, n - 1)];
+  };
+  auto look = [&](const auto& t, uint32_t n, uint32_t i0, int64_t begin, uint32_t most, auto f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < (int)(sizeof(t) / 8); ++k) {
+      const uint32_t i = i0 + k * THREADS + lane;
+      const uint64_t j = t[k] - (uint64_t)begin;
+      if (i < n && j < most) f((uint32_t)j, i);
+    }
+  };
+  // t: the history's first places, as asked for
+  auto mark_tokens = [&](uint64_t (&t)[kTokensAhead], int64_t begin, uint32_t most, uint32_t prompt_bit) __attribute__((always_inline)) {
+    constexpr uint32_t kStep = kTokensAhead * THREADS;
+    auto mark = [&](uint32_t j, uint32_t i) {
+      if (i >= answer) atomicAdd(&table[j], 1u);
+      else atomicOr(&table[j], prompt_bit);
+    };
+    if (hist.n <= kStep) {
+      look(t, hist.n, 0, begin, most, mark);
+      return;
+    }
+    // a long history: the next places are on their way while these are looked
+    // at, in two buffers by name (moving a loaded register to another waits
+    // for it) and without a branch (the last place again past the end)
+    uint64_t next[kTokensAhead];
+    auto ask_all = [&](uint64_t (&to)[kTokensAhead], uint32_t i0) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < kTokensAhead; ++k) to[k] = (uint64_t)tokens[min(i0 + k * THREADS + lane, hist.n - 1)];
+    };
+    for (uint32_t i0 = 0;;) {
+      ask_all(next, i0 + kStep);
+      look(t, hist.n, i0, begin, most, mark);
+      i0 += kStep;
+      if (i0 >= hist.n) break;
+      ask_all(t, i0 + kStep);
+      look(next, hist.n, i0, begin, most, mark);
+      i0 += kStep;
+      if (i0 >= hist.n) break;
+    }
+  };
+  auto store = [&]() __attribute__((always_inline)) {
+    // the mask on the elements as they are: a -infinity where a bit is 0
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-      const uint32_t u = i * kBlock + threadIdx.x;
-      if (u < full && mine(u)) {
-        float f[E];
-        widen_unit(z[i], f);
-        mark(u, f);
-        mask_out(u, f);
-        store_unit<DT, E, true>(to, u * E, narrow_unit<DT, E>(f));
+      const uint32_t u = i * THREADS + lane, allow = mask_bits(u * E, mw[i]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        auto all_of = [&](int bit) { return (uint32_t)((int32_t)(allow << (31 - bit)) >> 31); };
+        const uint32_t keep = DT == kF32 ? all_of(k) : (all_of(2 * k) & 0xffffu) | (all_of(2 * k + 1) & 0xffff0000u);
+        z[i].v[0][k] = (z[i].v[0][k] & keep) | ((DT == kF32 ? 0xff800000u : 0xff80ff80u) & ~keep);
       }
+      store_unit<DT, E, true>(to, u * E, z[i]);
     }
-    if (ends && mine(full)) {
-      float f[E];
-      widen_unit(last, f);
-      mark(full, f);
-      mask_out(full, f);
-      store_part<DT, E>(dst, full * E, part, f);
-    }
-  };
-  // Each entry of a list of n places in this run (of `most` entries from
-  // vocabulary index `begin` on): f(entry's place in the run, place in the list).
-  auto each = [&](const int64_t* list, uint32_t n, int64_t begin, uint32_t most, auto f) {
-    for (uint32_t i = threadIdx.x; i < n; i += kBlock) {
-      const uint64_t j = (uint64_t)list[i] - (uint64_t)begin;
-      if (j < most) f((uint32_t)j, i);
-    }
+    if (lane < part) reinterpret_cast<S*>(dst)[end] = mask_bits(end, end_mw) & 1 ? end_raw : narrow1<DT>(-__builtin_inff());
   };
 
   if (!hist.n && !bias.n) {
-    finish([](uint32_t) { return true; }, [](uint32_t, float (&)[E]) {});
-  } else if (hist.n <= kCountMost && bias.n <= kBiasPlaces) {
-    u32x4* t = reinterpret_cast<u32x4*>(table);
+    store();
+  } else if (hist.n <= kCountMost && bias.n <= kBiasMost) {
+    // the first of both lists are on their way while the table is cleared
+    uint64_t t[kTokensAhead], p[1];
+    ask(p, places, bias.n, 0);
+    float value = 0.0f;
+    if (bias.n) value = values[min(lane, bias.n - 1)];
+    ask(t, tokens, hist.n, 0);
+    u32x4* words = reinterpret_cast<u32x4*>(table);
 #pragma unroll
-    for (int i = 0; i < (int)(kRun / 4 / kBlock); ++i) t[i * kBlock + threadIdx.x] = u32x4{0, 0, 0, 0};
+    for (int i = 0; i < (int)(kRun / 4 / THREADS); ++i) words[i * THREADS + lane] = u32x4{0, 0, 0, 0};
     __syncthreads();
-    if (bias.n) {
-      each(places, bias.n, first, len, [&](uint32_t j, uint32_t i) { atomicMax(&table[j], (kBiasPlaces - i) << 16); });
-      __syncthreads();
+    for (uint32_t i0 = 0; i0 < bias.n;) {
+      look(p, bias.n, i0, first, len, [&](uint32_t j, uint32_t i) {
+        // the first place's bits, whatever else the word holds
+        const uint32_t bits = (kBiasMost - i) << kBiasShift;
+        for (uint32_t had = table[j]; had >> kBiasShift < bits >> kBiasShift;) {
+          const uint32_t now = atomicCAS(&table[j], had, bits | (had & kSeen));
+          if (now == had) break;
+          had = now;
+        }
+      });
+      i0 += THREADS;
+      ask(p, places, bias.n, i0);
     }
-    each(tokens, hist.n, first, len, [&](uint32_t j, uint32_t i) {
-      if (i >= answer) atomicAdd(&table[j], 1u);
-      else atomicOr(&table[j], kPrompt);
-    });
+    first_values[lane] = value;
+    mark_tokens(t, first, len, kPrompt);
     __syncthreads();
-    finish([](uint32_t) { return true; }, [&](uint32_t u, float (&f)[E]) {
-      uint32_t w[E], any = 0;
+    // Few units have an entry to adjust: a wave collects its own, and goes
+    // over them at once.
+    const uint32_t wave0 = lane / kWave * kWave;
+    uint32_t place[UNITS], n = 0;
+    bool hit[UNITS];
 #pragma unroll
-      for (int e = 0; e < E; ++e) any |= w[e] = table[u * E + e];
-      if (any) {
+    for (int i = 0; i < UNITS; ++i) {
+      uint32_t any = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          f[e] = penalize(f[e], w[e] & 0xffffu, w[e] & kCountMost);
-          if (w[e] >> 16) f[e] += values[kBiasPlaces - (w[e] >> 16)];
+      for (int e = 0; e < E; ++e) any |= table[(i * THREADS + lane) * E + e];
+      hit[i] = any != 0;
+      const unsigned long long m = __ballot(hit[i]);
+      place[i] = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+      n += (uint32_t)__popcll(m);
+    }
+    if (n > kWave) {
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i)
+        if (hit[i]) z[i] = adjust_unit(z[i], i * THREADS + lane);
+    } else if (n) {
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i) {
+        if (hit[i]) {
+          held[wave0 + place[i]] = z[i].v[0];
+          held_unit[wave0 + place[i]] = (uint16_t)(i * THREADS + lane);
         }
       }
-    });
+      wave_fence();
+      if (lane - wave0 < n) {
+        const RawUnit<DT, E> raw = {{held[lane]}};
+        held[lane] = adjust_unit(raw, held_unit[lane]).v[0];
+      }
+      wave_fence();
+#pragma unroll
+      for (int i = 0; i < UNITS; ++i)
+        if (hit[i]) z[i].v[0] = held[wave0 + place[i]];
+    }
+    if (lane < part) {
+      if (const uint32_t w = table[end]) end_raw = narrow1<DT>(adjust(widen1<DT>(end_raw), w));
+    }
+    store();
   } else {
-    // two words an entry: count and prompt, place of the bias
+    // two words an entry: count and prompt, place of the bias; entry by entry
+    // (going over so long a list takes longer)
     constexpr uint32_t kHalf = kRun / 2;
     uint32_t* where = table + kHalf;
-    for (uint32_t half = 0; half < 2; ++half) {
-      const int64_t begin = first + half * kHalf;
-      for (uint32_t i = threadIdx.x; i < kHalf; i += kBlock) {
+    for (uint32_t begin = 0; begin < len; begin += kHalf) {
+      for (uint32_t i = lane; i < kHalf; i += THREADS) {
         table[i] = 0;
         where[i] = ~0u;
       }
       __syncthreads();
-      each(places, bias.n, begin, kHalf, [&](uint32_t j, uint32_t i) { atomicMin(&where[j], i); });
-      each(tokens, hist.n, begin, kHalf, [&](uint32_t j, uint32_t i) {
-        if (i >= answer) atomicAdd(&table[j], 1u);
-        else atomicOr(&table[j], kLongPrompt);
-      });
+      uint64_t t[kTokensAhead], p[1];
+      for (uint32_t i0 = 0; i0 < bias.n; i0 += THREADS) {
+        ask(p, places, bias.n, i0);
+        look(p, bias.n, i0, first + begin, kHalf, [&](uint32_t j, uint32_t i) { atomicMin(&where[j], i); });
+      }
+      ask(t, tokens, hist.n, 0);
+      mark_tokens(t, first + begin, kHalf, kLongPrompt);
       __syncthreads();
-      finish([&](uint32_t u) { return u * E / kHalf == half; }, [&](uint32_t u, float (&f)[E]) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const uint32_t j = u * E - half * kHalf + e, w = table[j], k = where[j];
-          f[e] = penalize(f[e], w, w & ~kLongPrompt);
-          if (k != ~0u) f[e] += values[k];
-        }
-      });
+      for (uint32_t i = begin + lane; i < min(begin + kHalf, len); i += THREADS) {
+        const uint32_t w = table[i - begin], k = where[i - begin];
+        float v = penalize(widen1<DT>(reinterpret_cast<const S*>(src)[i]), w, w & ~kLongPrompt);
+        if (k != ~0u) v += values[k];
+        uint32_t m[2] = {~0u, ~0u};
+        if (a.mask) mask_words(i, 1, m);
+        reinterpret_cast<S*>(dst)[i] = narrow1<DT>(mask_bits(i, m) & 1 ? v : -__builtin_inff());
+      }
       __syncthreads();
     }
   }
 }
 
-// Units to a lane: four where that still gives the card's CUs some workgroups
-// each, which then go over a row's history the fewest times.
-constexpr uint64_t kManyRuns = 2048;
+// Runs of 2048 units where that still makes some 128 workgroups, else of 256:
+// bf16 rows of 131072 in 8 shards and histories of 4000, long and short runs:
+// 4 rows 9.0 and 7.1 us, 16 rows 8.7 and 9.7, 32 rows 9.0 and 15.0; 16 rows of
+// 50256 in 4 shards (64 long runs) 8.2 and 7.8.
+constexpr uint64_t kManyRuns = 128;
 
-template <int DT, int UNITS>
+// Workgroups go to the XCDs in turn: with enough rows the runs of one are kept
+// on one XCD, whose L2 then serves the row's history to all but the first.
+constexpr int kXcds = 8;
+constexpr uint64_t kSpreadRows = 64;
+
+template <int DT, int THREADS, int UNITS>
 int adjust_t(AdjustArgs a, hipStream_t s) {
-  constexpr int64_t kRun = (int64_t)UNITS * kBlock * kElems<DT>;
+  constexpr int64_t kRun = (int64_t)UNITS * THREADS * kElems<DT>;
   a.first[0] = 0;
   for (int r = 0; r < a.p; ++r) a.first[r + 1] = a.first[r] + (int)((a.first_index[r + 1] - a.first_index[r] + kRun - 1) / kRun);
   a.chunks = a.first[a.p];
   a.ranks_q32 = ((uint64_t)a.p << 32) / (uint64_t)a.chunks;
-  const uint64_t all = a.rows;
-  return over_rows(all, (uint64_t)a.chunks * (kBlock / kWave), [&](uint64_t first, uint64_t rows, dim3 grid) {
-    a.first_row = first;
-    a.rows = rows;
-    hipLaunchKernelGGL((adjust_kernel<DT, UNITS>), grid, dim3(kBlock), 0, s, a);
-  });
+  a.spread = a.offsets && a.rows >= kSpreadRows ? kXcds : 1;
+  const uint64_t all = a.rows, most = most_blocks(THREADS) / (uint64_t)a.chunks / kXcds * kXcds;
+  for (a.first_row = 0; a.first_row < all; a.first_row += most) {
+    a.rows = std::min(most, all - a.first_row);
+    const uint64_t groups = (a.rows + a.spread - 1) / a.spread;
+    hipLaunchKernelGGL((adjust_kernel<DT, THREADS, UNITS>), dim3((uint32_t)(groups * a.spread * a.chunks)), dim3(THREADS), 0, s, a);
+    if (const int e = (int)hipGetLastError()) return e;
+  }
+  return 0;
 }
 
 template <int DT>
 int adjust_d(const AdjustArgs& a, hipStream_t s) {
-  constexpr uint64_t kLong = 4 * kBlock * kElems<DT>;
+  constexpr uint64_t kLong = 2048 * kElems<DT>;
   uint64_t runs = 0;
   for (int r = 0; r < a.p; ++r) runs += ((uint64_t)(a.first_index[r + 1] - a.first_index[r]) + kLong - 1) / kLong;
-  return a.rows >= (kManyRuns + runs - 1) / runs ? adjust_t<DT, 4>(a, s) : adjust_t<DT, 1>(a, s);
+  return a.rows >= (kManyRuns + runs - 1) / runs ? adjust_t<DT, 512, 4>(a, s) : adjust_t<DT, 256, 1>(a, s);
 }
 
 }  // namespace

@@ -176,12 +176,6 @@ __device__ __forceinline__ float bar_of(float mine, int top) {
   return fmaxf(wave_max(reached >= top ? mine : -FLT_MAX), -FLT_MAX);
 }
 
-// LDS is written and read by one wave alone.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Entries that a wave collects in LDS; n counts also those past its end.
 template <class T, uint32_t MOST>
 struct Bag {

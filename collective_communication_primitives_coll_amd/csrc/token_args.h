@@ -196,7 +196,8 @@ struct AdjustArgs {
   int64_t old[kMaxRanks];
   int64_t first_index[kMaxRanks + 1];  // first vocabulary index of each shard, and the end
   int first[kMaxRanks + 1];      // first run of each shard's rows, and the end (set by the launcher)
-  int chunks;                    // runs of a row
+  int chunks;                    // runs of a row (set by the launcher)
+  int spread;                    // rows whose runs take turns (set by the launcher)
   uint64_t ranks_q32;            // ranks to a run on average, times 2^32
   const int64_t* tokens;         // [ntokens], row r's from offsets[r] to offsets[r + 1]
   const int64_t* offsets;

@@ -67,6 +67,12 @@ __device__ __forceinline__ RawUnit<DT, kElems<DT>> masked_unit() {
   return RawUnit<DT, kElems<DT>>{{u32x4{w, w, w, w}}};
 }
 
+// LDS is written and read by one wave alone.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 template <int N>
 __device__ __forceinline__ float largest(const float (&f)[N]) {
   float v = f[0];

@@ -108,7 +108,8 @@ def test_each_part_alone(coll, parts, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("longest,list_length", [(32767, 3), (32768, 3), (100000, 40), (5, 65535), (5, 65536), (40000, 70000)])
+@pytest.mark.parametrize("longest,list_length", [(32767, 3), (32768, 3), (100000, 40), (5, 65535), (5, 65536), (40000, 70000),
+                                                  (1048575, 2), (1048576, 2), (5, 2047), (5, 2048)])
 @pytest.mark.parametrize("rows", [3, 300])
 def test_long_histories_and_lists(coll, longest, list_length, rows, dtype):
     """Either side of what a table of one word an entry holds, in runs of either length."""
