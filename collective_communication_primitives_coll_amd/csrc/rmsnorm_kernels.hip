@@ -50,18 +50,28 @@ __device__ __forceinline__ RawUnit<DT, E> add_units(const RawUnit<DT, E>& a, con
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  Grid (runs of rows, ranks), no walk, two rows to a lane, and the
-// weights asked for after the sums, as in layer norm.  h is stored after the
-// sums too: it may replace x or the residual, whose rows of an odd width have
-// lanes that share elements.
+// Forward.  Grid (runs of rows, ranks), no walk, and the weights asked for
+// after the sums, as in layer norm.  h is stored after the sums too: it may
+// replace x or the residual, whose rows of an odd width have lanes that share
+// elements.  8 x 4096 x 7168 bf16 with a residual: 308 us (6.1 TB/s; 1:1 streams
+// reach 6.24), without 151 us; to 8 bits 270 and 123 us.
 // ---------------------------------------------------------------------------
-template <int DT, int TPR>
-constexpr int rows_of() { return TPR == 1024 && DT == kBF16 ? 1 : 2; }
+// Rows to a lane: one where a row with its residual, or half a workgroup's lanes
+// and more, keep enough loads in flight.  us with one row and with two, bf16
+// with a residual: 8 x 4096 x 8192 353 and 370, 4096 174 and 176, 2560 114 and
+// 111, 8 x 131072 x 64 96 and 80; fp32 8 x 2048 x 7168 329 and 336, 4096 176 and
+// 185; without: bf16 8 x 4096 x 8192 170 and 178, 5120 110 and 107, in 8 bits
+// 7168 131 and 123.
+template <int DT, int TPR, bool RES, bool FP8>
+constexpr int rows_of() {
+  if (TPR == 1024 && DT == kBF16) return 1;
+  return (RES ? TPR >= (DT == kF32 ? 192 : 256) : TPR >= 512 && !FP8) ? 1 : 2;
+}
 
 template <int DT, int WT, int TPR, int NU, bool TAIL, bool RES, bool FP8>
 __global__ __launch_bounds__(block_of(TPR)) void rms_forward_kernel(RmsArgs a) {
   constexpr int E = kElems<DT>;
-  constexpr int kRows = rows_of<DT, TPR>();
+  constexpr int kRows = rows_of<DT, TPR, RES, FP8>();
   __shared__ float red[2][kRows][waves_of(TPR)];
   const int rank = blockIdx.y;
   const uint32_t lane = threadIdx.x % TPR, H = (uint32_t)a.hidden;
@@ -230,7 +240,35 @@ __global__ __launch_bounds__(1024) void rms_forward_wide_kernel(RmsArgs a) {
 // ---------------------------------------------------------------------------
 // Backward.  A workgroup takes every gridDim.x-th run of rows, through all
 // ranks of the launch, and writes its partial sums to ws[blockIdx.x][hidden].
+// h and dy are asked for one row ahead; dh, which is needed last, with its own
+// row: the card works best in a narrow window of memory (8 x 4096 x 7168 bf16:
+// 307 us, 6.1 TB/s, and 321 with dh a row ahead as well; two rows ahead 321).
 // ---------------------------------------------------------------------------
+// Whether dx is written through the L2 at once (device scope) rather than past
+// it (non-temporal).  By lanes to a row, us of either with a residual, bf16:
+// 256 lanes (4096 columns) 171 and 186, 384 (5120) 114 and 119, 512 (7168) 319
+// and 307, 768 (12288) 289 and 281, 1024 (16384) 371 and 367.
+template <int TPR>
+constexpr bool kWriteThrough = TPR >= kWave && TPR <= 384;
+
+// Units of dx.  The base is the same on every lane that shares a buffer.
+template <int DT, int E, int TPR, bool TAIL>
+struct DxRow {
+  RowBuffer b;
+  Row<DT, E, TAIL> row;
+  uint32_t last;  // first element of the row's last E
+  __device__ __forceinline__ DxRow(void* base, uint32_t hidden)
+      : b(base, kWriteThrough<TPR> ? hidden * Traits<DT>::B : 0), row(base, hidden), last(hidden - E) {}
+  __device__ __forceinline__ void put(uint32_t u, const RawUnit<DT, E>& r) const {
+    if constexpr (kWriteThrough<TPR>) {
+      const uint32_t at = TAIL ? min(E * u, last) : E * u;
+      __builtin_amdgcn_raw_buffer_store_b128(r.v[0], b.rsrc, (int)(at * Traits<DT>::B), 0, kCachePolicySc1);
+    } else {
+      row.template put<true>(u, r);
+    }
+  }
+};
+
 template <int DT, int WT, int TPR, int NU, bool TAIL, bool DH>
 __global__ __launch_bounds__(block_of(TPR)) void rms_backward_kernel(RmsArgs a) {
   constexpr int E = kElems<DT>, RPB = block_of(TPR) / TPR, AHEAD = kAhead<TPR>;
@@ -256,7 +294,7 @@ __global__ __launch_bounds__(block_of(TPR)) void rms_backward_kernel(RmsArgs a) 
   if (at.rank < a.ranks) {
     // AHEAD + 1 buffers; the loop is unrolled over them, since moving a
     // loaded register to another waits for its load
-    RawUnit<DT, E> bh[AHEAD + 1][NU], bd[AHEAD + 1][NU], br[AHEAD + 1][DH ? NU : 1];
+    RawUnit<DT, E> bh[AHEAD + 1][NU], bd[AHEAD + 1][NU], br[DH ? NU : 1];
     float bs[AHEAD + 1];
     auto fetch = [&](const Place& r, auto K) {
       constexpr int k = decltype(K)::value;
@@ -267,11 +305,6 @@ __global__ __launch_bounds__(block_of(TPR)) void rms_backward_kernel(RmsArgs a) 
       for (int i = 0; i < NU; ++i) {
         bh[k][i] = rh.template get<true>(i * TPR + lane);
         bd[k][i] = rd.template get<true>(i * TPR + lane);
-      }
-      if constexpr (DH) {
-        const Row<DT, E, TAIL> rr(static_cast<const uint8_t*>(a.res[r.rank]) + off, H);
-#pragma unroll
-        for (int i = 0; i < NU; ++i) br[k][i] = rr.template get<true>(i * TPR + lane);
       }
       bs[k] = ld_const(a.rstd[r.rank] + r.row);
     };
@@ -295,6 +328,11 @@ __global__ __launch_bounds__(block_of(TPR)) void rms_backward_kernel(RmsArgs a) 
       next.settle(a);
       const bool more = next.rank < a.ranks;
       if (!more) next = at;
+      if constexpr (DH) {
+        const Row<DT, E, TAIL> rr(static_cast<const uint8_t*>(a.res[at.rank]) + at.row * row_bytes, H);
+#pragma unroll
+        for (int i = 0; i < NU; ++i) br[i] = rr.template get<true>(i * TPR + lane);
+      }
       if constexpr (AHEAD > 0) fetch(next, std::integral_constant<int, (k + 1) % (AHEAD + 1)>());
       const float rstd = bs[k];
       float n[NU][E], w[NU][E], s[1] = {0.0f};
@@ -317,14 +355,14 @@ __global__ __launch_bounds__(block_of(TPR)) void rms_backward_kernel(RmsArgs a) 
       row_sums<TPR, 1>(s, red[turn]);
       turn ^= 1;
       const float c = s[0] / (float)H;
-      const Row<DT, E, TAIL> dx(static_cast<uint8_t*>(a.y[at.rank]) + at.row * row_bytes, H);
+      const DxRow<DT, E, TPR, TAIL> dx(static_cast<uint8_t*>(a.y[at.rank]) + at.row * row_bytes, H);
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         float r[E];
-        if constexpr (DH) widen_unit(br[k][i], r);
+        if constexpr (DH) widen_unit(br[i], r);
 #pragma unroll
         for (int e = 0; e < E; ++e) w[i][e] = rstd * (w[i][e] - n[i][e] * c) + (DH ? r[e] : 0.0f);
-        dx.template put<true>(i * TPR + lane, narrow_unit<DT, E>(w[i]));
+        dx.put(i * TPR + lane, narrow_unit<DT, E>(w[i]));
       }
       if constexpr (AHEAD == 0) fetch(next, K);
       at = next;
@@ -473,7 +511,7 @@ int forward_t(const RmsArgs& a, hipStream_t s) {
   return with_shape(tpr, nu, [&](auto T, auto N) {
     constexpr int TPR = decltype(T)::value, NU = decltype(N)::value * 8 / kElems<DT>, RPB = block_of(TPR) / TPR;
     constexpr bool PACKED = TPR < kWave;  // several rows to a wave
-    const uint64_t run = RPB * rows_of<DT, TPR>();
+    const uint64_t run = RPB * rows_of<DT, TPR, RES, FP8>();
     const dim3 block(block_of(TPR));
     const uint64_t most = most_blocks(block.x) * run;
     RmsArgs part = a;
@@ -505,8 +543,8 @@ int backward_t(const RmsArgs& a, uint32_t groups, hipStream_t s) {
   }
   return with_shape(tpr, nu, [&](auto T, auto N) {
     constexpr int TPR = decltype(T)::value, NU = decltype(N)::value * 8 / kElems<DT>;
-    constexpr bool PACKED = TPR < kWave;
     const dim3 grid(groups), block(block_of(TPR));
+    constexpr bool PACKED = TPR < kWave;
     if (PACKED || a.hidden % kElems<DT>) hipLaunchKernelGGL((rms_backward_kernel<DT, WT, TPR, NU, true, DH>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((rms_backward_kernel<DT, WT, TPR, NU, PACKED, DH>), grid, block, 0, s, a);
     return (int)hipGetLastError();
@@ -526,8 +564,18 @@ int backward_w(const RmsArgs& a, bool dh, uint32_t groups, hipStream_t s) {
 }  // namespace
 
 // Workgroups of a launch of the backward pass: by the shape alone (results
-// and workspace must not depend on the device or on the grid limit).
-uint32_t rms_backward_groups(int p, uint64_t rows, uint64_t hidden) { return ln_backward_groups(p, rows, hidden); }
+// and workspace must not depend on the device or on the grid limit).  As in
+// layer norm, but for rows of 128 columns and fewer, whose steps are short:
+// with 1024 and 512 workgroups 8 x 65536 x 128 bf16 took 102 and 132 us (fp32
+// 185 and 184), 8 x 131072 x 64 150 and 216 (fp32 215 and 251).
+constexpr uint64_t kNarrowGroups = 1024;
+uint32_t rms_backward_groups(int p, uint64_t rows, uint64_t hidden) {
+  int tpr, nu;
+  row_shape(hidden, &tpr, &nu);
+  if (tpr != 16 || nu != 1) return ln_backward_groups(p, rows, hidden);
+  const uint64_t rpb = kBlock / 16, need = (rows * (uint64_t)std::min(p, kArgRanks) + rpb - 1) / rpb;
+  return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(need, kNarrowGroups));
+}
 
 int launch_rms_forward(int dtype, int wdtype, const RmsArgs& a, bool residual, bool fp8, void* stream) {
   hipStream_t s = (hipStream_t)stream;
