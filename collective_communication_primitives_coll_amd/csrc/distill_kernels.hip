@@ -167,10 +167,39 @@ __global__ __launch_bounds__(kBlock) void distill_pieces_kernel(DistillArgs a) {
     if (en.at[k] != ~0u) as_global(a.zs)[row * (uint64_t)a.top + k * kWave + lane] = widen1<DT>(z_raw[k]);
 }
 
-__device__ __forceinline__ double wave_sum64(double v) {
+// Sums of 64-bit values over a wave, on every lane, in wave_fold's order; N at
+// once, whose steps hide each other's latency.
+__device__ __forceinline__ double halves(uint32_t lo, uint32_t hi) { return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo); }
+template <int CTRL>
+__device__ __forceinline__ double dpp_move(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return halves((uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xf, 0xf, false),
+                (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf, false));
+}
+template <int N>
+__device__ __forceinline__ void wave_sums64(double (&v)[N]) {
 #pragma unroll
-  for (int m = 1; m < kWave; m *= 2) v += __shfl_xor(v, m);
-  return v;
+  for (int k = 0; k < N; ++k) v[k] += dpp_move<0xB1>(v[k]);   // quad_perm 1,0,3,2
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] += dpp_move<0x4E>(v[k]);   // quad_perm 2,3,0,1
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] += dpp_move<0x141>(v[k]);  // row_half_mirror
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] += dpp_move<0x140>(v[k]);  // row_mirror
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v[k]);
+    const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+    v[k] = halves(lo[0], hi[0]) + halves(lo[1], hi[1]);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v[k]);
+    const auto lo = __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false);
+    const auto hi = __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+    v[k] = halves(lo[0], hi[0]) + halves(lo[1], hi[1]);
+  }
 }
 
 // A wave to a row, a lane to a piece and to one or two entries.
@@ -181,6 +210,8 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillJoinArgs a)
   const uint32_t in = blockIdx.x * (kBlock / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (in >= a.rows) return;
   const uint64_t row = a.first_row + in;
+  // (asked for first: needed last)
+  float *stats = a.stats[min(lane, a.p - 1)], *losses = a.loss[min(lane, a.p - 1)];
   RunningSum run;
   if (lane < a.pieces) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -199,7 +230,8 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillJoinArgs a)
     if (l[k] == inf) l[k] = nan;
     const bool ok = id[k] >= 0 && id[k] < a.vocab;
     if (!ok) id[k] = -1;
-    z[k] = ok ? as_global(a.zs)[at] : -inf;
+    const float zi = as_global(a.zs)[at];  // (not written where the entry is in no shard)
+    z[k] = ok ? zi : -inf;
   }
   // an index's first entry counts
   bool again[NT] = {};
@@ -224,47 +256,39 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillJoinArgs a)
   run.rebase(mt, c);
   const float st = wave_sum(run.s);
   const double scale = a.scale;
-  float m = mt;
-  double sum = st, third = 0.0, fourth = 0.0, q[NT];
+  // Over the entries, with e their masses (about the largest where they are to
+  // be normalised) and d the student's exponents: sum e, sum e (l - d), and with
+  // a tail sum e^d.  The loss then only wants the logarithms of sums.
+  float m = mt, lm = -inf;
+#pragma unroll
+  for (int k = 0; k < NT; ++k) {
+    if (a.tail) m = fmaxf(m, counts[k] ? z[k] : -inf);
+    else lm = fmaxf(lm, counts[k] ? l[k] : -inf);
+  }
+  m = wave_max(m);
+  lm = a.tail ? 0.0f : wave_max(lm);
+  double s[3] = {0.0, 0.0, 0.0};
+#pragma unroll
+  for (int k = 0; k < NT; ++k) {
+    const double d = ((double)z[k] - m) * scale, e = counts[k] ? exp((double)l[k] - lm) : 0.0;
+    s[0] += e;
+    s[1] += e == 0.0 ? 0.0 : e * (l[k] - d);
+    s[2] += counts[k] ? exp(d) : 0.0;
+  }
+  const double far = ((double)mt - m) * scale;
+  double third = log((double)st) + far, fourth = 0.0, sum = st == 0.0f ? 0.0 : st * exp(far);
+  wave_sums64(s);
   if (a.tail) {
-#pragma unroll
-    for (int k = 0; k < NT; ++k) m = fmaxf(m, counts[k] ? z[k] : -inf);
-    m = wave_max(m);
-    const double far = ((double)mt - m) * scale;
-    double inside = 0.0, mass = 0.0;
-#pragma unroll
-    for (int k = 0; k < NT; ++k) {
-      q[k] = counts[k] ? exp((double)l[k]) : 0.0;
-      mass += q[k];
-      inside += counts[k] ? exp(((double)z[k] - m) * scale) : 0.0;
-    }
-    inside = wave_sum64(inside);
-    sum = inside + (st == 0.0f ? 0.0 : st * exp(far));
-    third = log((double)st) + far;
+    sum += s[2];
     if (third < kNone) third = -inf;  // (also of an empty sum)
-    fourth = 1.0 - wave_sum64(mass);
+    fourth = 1.0 - s[0];
   } else {
-    float lm = -inf;
-#pragma unroll
-    for (int k = 0; k < NT; ++k) lm = fmaxf(lm, counts[k] ? l[k] : -inf);
-    lm = wave_max(lm);
-    double mass = 0.0;
-#pragma unroll
-    for (int k = 0; k < NT; ++k) mass += counts[k] ? exp((double)l[k] - lm) : 0.0;
-    third = log(wave_sum64(mass)) + lm;
-#pragma unroll
-    for (int k = 0; k < NT; ++k) q[k] = counts[k] ? exp((double)l[k] - third) : 0.0;
+    third = log(s[0]) + lm;
   }
   // (comparisons that a NaN fails)
   const bool poison = !(sum >= 0.0), empty = sum == 0.0;
   const double log_s = log(sum);
-  double loss = 0.0;
-#pragma unroll
-  for (int k = 0; k < NT; ++k) {
-    const double lq = a.tail ? (double)l[k] : l[k] - third, lp = ((double)z[k] - m) * scale - log_s;
-    loss += q[k] == 0.0 ? 0.0 : q[k] * (lq - lp);
-  }
-  loss = wave_sum64(loss);
+  double loss = a.tail ? s[1] + (s[0] == 0.0 ? 0.0 : s[0] * log_s) : s[1] / s[0] - third + log_s;
   if (a.tail && !(fourth <= 0.0) && third != -inf) loss += fourth * (log(fourth) - (third - log_s));
   if (lane < a.p) {
     typedef float f32x4_e __attribute__((ext_vector_type(4), aligned(4)));
@@ -274,8 +298,8 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillJoinArgs a)
     // one NaN on every rank, whatever lane it comes from
     out[2] = !any ? inf : poison || third != third ? nan : (float)third;
     out[3] = !any ? 0.0f : poison || fourth != fourth ? nan : (float)fourth;
-    *reinterpret_cast<f32x4_e*>(as_global(a.stats[lane]) + row * 4) = out;
-    as_global(a.loss[lane])[row] = !any ? 0.0f : poison ? nan : empty ? inf : loss != loss ? nan : (float)loss;
+    *reinterpret_cast<f32x4_e*>(as_global(stats) + row * 4) = out;
+    as_global(losses)[row] = !any ? 0.0f : poison ? nan : empty ? inf : loss != loss ? nan : (float)loss;
   }
 }
 
