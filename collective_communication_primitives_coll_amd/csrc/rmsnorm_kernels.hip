@@ -352,6 +352,14 @@ __global__ __launch_bounds__(block_of(TPR)) void rms_backward_kernel(RmsArgs a) 
           s[0] += own ? w[i][e] * n[i][e] : 0.0f;
         }
       }
+      if (DH && TAIL && H % E) {
+        // dx may take dh's place, and lanes of a row of an odd width share
+        // elements: dh has arrived on every wave before any of them stores
+#pragma unroll
+        for (int i = 0; i < NU; ++i)
+#pragma unroll
+          for (auto& v : br[i].v) asm volatile("" : "+v"(v));
+      }
       row_sums<TPR, 1>(s, red[turn]);
       turn ^= 1;
       const float c = s[0] / (float)H;

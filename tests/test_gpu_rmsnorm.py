@@ -135,6 +135,27 @@ def test_in_place_forms_give_the_same_bits(coll, hidden, dtype):
     assert all(torch.equal(u, v) for u, v in zip(dx, dx2))
 
 
+@pytest.mark.parametrize("dtype,hidden", [(BF16, 2049), (BF16, 4097), (BF16, 6145), (BF16, 137), (F32, 1025), (F32, 2561), (F32, 8193)])
+def test_gradient_in_place_of_rows_whose_waves_share_elements(coll, dtype, hidden):
+    """The row's last, partial unit begins a wave, whose lane shares elements with the wave before."""
+    import torch
+    g = rng(57, hidden, dtype)
+    p, rows = 2, 2000
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(hidden)
+    dy, dh, h = [[torch.randn(rows, hidden, generator=gen, device="cuda").to({F32: torch.float32, BF16: torch.bfloat16}[dtype]) for _ in range(p)] for _ in range(3)]
+    gamma = [dev(g.normal(1, 0.2, hidden), F32)[0]] * p
+    rstd = torch.rand(p, rows, generator=gen, device="cuda") + 0.5
+    ws = workspace(coll.coll_rmsnorm_workspace_bytes(p, rows, hidden))
+    dx, dg, dg2 = [new((rows, hidden), dtype) for _ in range(p)], f32(p, hidden), f32(p, hidden)
+    coll.coll_rmsnorm_backward(dy, h, list(rstd), gamma, dx, list(dg), ws, hidden, dh=dh)
+    for place in ("dy", "dh"):
+        a, b = [t.clone() for t in dy], [t.clone() for t in dh]
+        out = a if place == "dy" else b
+        coll.coll_rmsnorm_backward(a, h, list(rstd), gamma, out, list(dg2), ws, hidden, dh=b)
+        assert all(torch.equal(u, v) for u, v in zip(dx, out)) and torch.equal(dg, dg2), place
+
+
 def test_backward_of_no_rows_writes_zeros(coll):
     dg = f32(2, 40)
     coll.coll_rmsnorm_backward([0, 0], [0, 0], [0, 0], None, [0, 0], list(dg), 0, 40, rows=0, dtype=F32, wdtype=F32, workspace_bytes=0)
