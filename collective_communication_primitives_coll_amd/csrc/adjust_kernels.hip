@@ -325,8 +325,10 @@ int adjust_t(AdjustArgs a, hipStream_t s) {
   for (int r = 0; r < a.p; ++r) a.first[r + 1] = a.first[r] + (int)((a.first_index[r + 1] - a.first_index[r] + kRun - 1) / kRun);
   a.chunks = a.first[a.p];
   a.ranks_q32 = ((uint64_t)a.p << 32) / (uint64_t)a.chunks;
-  a.spread = a.offsets && a.rows >= kSpreadRows ? kXcds : 1;
-  const uint64_t all = a.rows, most = most_blocks(THREADS) / (uint64_t)a.chunks / kXcds * kXcds;
+  // (a row has 2^21 + 63 runs at most, so that a launch holds one)
+  const uint64_t all = a.rows, rows = most_blocks(THREADS) / (uint64_t)a.chunks;
+  a.spread = a.offsets && std::min(all, rows) >= kSpreadRows ? kXcds : 1;
+  const uint64_t most = rows / (uint64_t)a.spread * (uint64_t)a.spread;
   for (a.first_row = 0; a.first_row < all; a.first_row += most) {
     a.rows = std::min(most, all - a.first_row);
     const uint64_t groups = (a.rows + a.spread - 1) / a.spread;

@@ -626,7 +626,7 @@ coll_status_t coll_vocab_logprob_backward(const void* const* logits, const int64
  *   repetition, presence, frequency   fp32 [rows]: with c_j the number of
  *               times that token j is among the answer's,
  *                 z_j > 0 ? z_j / repetition : z_j repetition   where the
- *                                                history has token j,
+ *                                   history has token j (by the reciprocal),
  *                 z_j - (c_j frequency + presence)   where c_j > 0;
  *   bias_idx, bias, nbias, bias_offsets   int64, fp32, and offsets as above
  *               (nbias < 2^31): added to the entries that row r's part lists.

@@ -84,7 +84,8 @@ def test_binding_refuses_before_the_call():
 
 @host_only
 def test_launches_hold_the_work_items_that_hip_takes(tmp_path):
-    shapes = [(64, 1 << 20, 1), (64, (1 << 20) + 3, 16), (1, 1 << 26, 8), (1, (1 << 28) + 1, 100), (8, 1 << 20, 16384), (1, 3, 0x7fffffff), (1, 1 << 18, 131072)]
+    shapes = [(64, 1 << 20, 1), (64, (1 << 20) + 3, 16), (1, 1 << 26, 8), (1, (1 << 28) + 1, 100), (8, 1 << 20, 16384), (1, 3, 0x7fffffff), (64, 100, (1 << 25) - 1),
+              (1, 1 << 18, 131072)]
     calls = []
     for p, rows, v in shapes:
         one = f"_i64(*[{v}] * {p})"
