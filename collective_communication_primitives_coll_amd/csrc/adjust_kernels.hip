@@ -18,7 +18,9 @@
 // 512 x 131072 bf16 in 8 shards, masks, 100 biases and histories of 4000
 // tokens on average (most shorter, some of 30000 and more): 72 us; 67 with
 // 4000 in every row, 59 without masks and biases, 48 with nothing to mark
-// (5.6 TB/s).  Runs of 8192 entries took 73 for 67, and 82 where a row's runs
+// (5.6 TB/s): what marks cost is the instructions of going over the history
+// and of the units to adjust (570 a wave, 330 without masks and biases), not
+// waiting: asking for the next tokens while these are looked at changed nothing.  Runs of 8192 entries took 73 for 67, and 82 where a row's runs
 // went to all XCDs; every lane adjusting its own units 85.  Where few rows
 // leave CUs without work, runs are short: 4 rows of 131072, 400 tokens: 5.4 us.
 //
@@ -52,7 +54,7 @@ struct Span {
   }
 };
 
-// Tokens that a lane asks for at a time; the next ones while it looks at these.
+// Tokens that a lane asks for at a time.
 constexpr int kTokensAhead = 8;
 
 template <int DT, int THREADS, int UNITS>
@@ -78,6 +80,22 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
   const uint8_t* src = as_global(static_cast<const uint8_t*>(a.logits[r])) + ((int64_t)row * a.ld[r] + at) * B;
   uint8_t* dst = as_global(static_cast<uint8_t*>(a.out[r])) + ((int64_t)row * a.old[r] + at) * B;
   const Span hist(a.offsets, row, a.ntokens), bias(a.bias_offsets, row, a.nbias);
+  const int64_t* tokens = as_global(a.tokens) + hist.begin;
+  const int64_t* places = as_global(a.bias_idx) + bias.begin;
+  const float* values = as_global(a.bias) + bias.begin;
+  // A list of n places in the vocabulary, from place i0 on, a lane's in t.  The
+  // first of both lists are asked for before the logits: loads return in
+  // order, and these are needed first.
+  auto ask = [&](auto& t, const int64_t* all, uint32_t n, uint32_t i0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < (int)(sizeof(t) / 8); ++k)
+      if (i0 + k * THREADS < n) t[k] = (uint64_t)all[min(i0 + k * THREADS + lane, n - 1)];
+  };
+  uint64_t t[kTokensAhead], p[1];
+  float value = 0.0f;
+  ask(p, places, bias.n, 0);
+  if (bias.n) value = values[min(lane, bias.n - 1)];
+  ask(t, tokens, hist.n, 0);
   const RowBuffer from(src, full * 16), to(dst, full * 16);
   RawUnit<DT, E> z[UNITS];
 #pragma unroll
@@ -110,9 +128,6 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
 
   const int64_t prompt = a.prompt ? ld_const(a.prompt + row) : 0;
   const uint32_t answer = prompt < 0 ? 0 : (uint32_t)min(prompt, (int64_t)hist.n);  // where the answer starts
-  const int64_t* tokens = as_global(a.tokens) + hist.begin;
-  const int64_t* places = as_global(a.bias_idx) + bias.begin;
-  const float* values = as_global(a.bias) + bias.begin;
   const float repetition = a.repetition ? ld_const(a.repetition + row) : 1.0f, inverse = 1.0f / repetition;
   const float presence = a.presence ? ld_const(a.presence + row) : 0.0f;
   const float frequency = a.frequency ? ld_const(a.frequency + row) : 0.0f;
@@ -143,14 +158,8 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
     }
     return narrow_unit<DT, E>(f);
   };
-  // A list of n places in the vocabulary, from place i0 on, a lane's in t; and
-  // those of them in this run (of `most` entries from vocabulary index `begin`
-  // on): f(entry's place in the run, place in the list).
-  auto ask = [&](auto& t, const int64_t* all, uint32_t n, uint32_t i0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int k = 0; k < (int)(sizeof(t) / 8); ++k)
-      if (i0 + k * THREADS < n) t[k] = (uint64_t)all[min(i0 + k * THREADS + lane, n - 1)];
-  };
+  // Those of a list's places in this run (of `most` entries from vocabulary
+  // index `begin` on): f(entry's place in the run, place in the list).
   auto look = [&](const auto& t, uint32_t n, uint32_t i0, int64_t begin, uint32_t most, auto f) __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < (int)(sizeof(t) / 8); ++k) {
@@ -161,32 +170,13 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
   };
   // t: the history's first places, as asked for
   auto mark_tokens = [&](uint64_t (&t)[kTokensAhead], int64_t begin, uint32_t most, uint32_t prompt_bit) __attribute__((always_inline)) {
-    constexpr uint32_t kStep = kTokensAhead * THREADS;
-    auto mark = [&](uint32_t j, uint32_t i) {
-      if (i >= answer) atomicAdd(&table[j], 1u);
-      else atomicOr(&table[j], prompt_bit);
-    };
-    if (hist.n <= kStep) {
-      look(t, hist.n, 0, begin, most, mark);
-      return;
-    }
-    // a long history: the next places are on their way while these are looked
-    // at, in two buffers by name (moving a loaded register to another waits
-    // for it) and without a branch (the last place again past the end)
-    uint64_t next[kTokensAhead];
-    auto ask_all = [&](uint64_t (&to)[kTokensAhead], uint32_t i0) __attribute__((always_inline)) {
-#pragma unroll
-      for (int k = 0; k < kTokensAhead; ++k) to[k] = (uint64_t)tokens[min(i0 + k * THREADS + lane, hist.n - 1)];
-    };
-    for (uint32_t i0 = 0;;) {
-      ask_all(next, i0 + kStep);
-      look(t, hist.n, i0, begin, most, mark);
-      i0 += kStep;
-      if (i0 >= hist.n) break;
-      ask_all(t, i0 + kStep);
-      look(next, hist.n, i0, begin, most, mark);
-      i0 += kStep;
-      if (i0 >= hist.n) break;
+    for (uint32_t i0 = 0; i0 < hist.n;) {
+      look(t, hist.n, i0, begin, most, [&](uint32_t j, uint32_t i) {
+        if (i >= answer) atomicAdd(&table[j], 1u);
+        else atomicOr(&table[j], prompt_bit);
+      });
+      i0 += kTokensAhead * THREADS;
+      ask(t, tokens, hist.n, i0);
     }
   };
   auto store = [&]() __attribute__((always_inline)) {
@@ -208,15 +198,9 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
   if (!hist.n && !bias.n) {
     store();
   } else if (hist.n <= kCountMost && bias.n <= kBiasMost) {
-    // the first of both lists are on their way while the table is cleared
-    uint64_t t[kTokensAhead], p[1];
-    ask(p, places, bias.n, 0);
-    float value = 0.0f;
-    if (bias.n) value = values[min(lane, bias.n - 1)];
-    ask(t, tokens, hist.n, 0);
-    u32x4* words = reinterpret_cast<u32x4*>(table);
+    u32x4* cleared = reinterpret_cast<u32x4*>(table);
 #pragma unroll
-    for (int i = 0; i < (int)(kRun / 4 / THREADS); ++i) words[i * THREADS + lane] = u32x4{0, 0, 0, 0};
+    for (int i = 0; i < (int)(kRun / 4 / THREADS); ++i) cleared[i * THREADS + lane] = u32x4{0, 0, 0, 0};
     __syncthreads();
     for (uint32_t i0 = 0; i0 < bias.n;) {
       look(p, bias.n, i0, first, len, [&](uint32_t j, uint32_t i) {
@@ -286,7 +270,6 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
         where[i] = ~0u;
       }
       __syncthreads();
-      uint64_t t[kTokensAhead], p[1];
       for (uint32_t i0 = 0; i0 < bias.n; i0 += THREADS) {
         ask(p, places, bias.n, i0);
         look(p, bias.n, i0, first + begin, kHalf, [&](uint32_t j, uint32_t i) { atomicMin(&where[j], i); });
