@@ -16,8 +16,8 @@
 // first.  Few units have a mark: a wave collects its own from its lanes and
 // adjusts them at once, before the mask, which needs no arithmetic.
 // 512 x 131072 bf16 in 8 shards, masks, 100 biases and histories of 4000
-// tokens on average (most shorter, some of 30000 and more): 72 us; 67 with
-// 4000 in every row, 59 without masks and biases, 48 with nothing to mark
+// tokens on average (most shorter, some of 30000 and more): 69-75 us; 67 with
+// 4000 in every row, 61 without masks and biases, 48 with nothing to mark
 // (5.6 TB/s): what marks cost is the instructions of going over the history
 // and of the units to adjust (570 a wave, 330 without masks and biases), not
 // waiting: asking for the next tokens while these are looked at changed nothing.  Runs of 8192 entries took 73 for 67, and 82 where a row's runs
@@ -32,12 +32,18 @@ namespace coll {
 
 namespace {
 
-// A table word of an entry: its count among the answer's tokens (bits 0..19),
-// whether the prompt has it (bit 20), and kBiasMost less the place of its bias
-// in the row's list (bits 21..31; 0: none).  Longer histories and lists take
-// two words an entry, and the run in two halves.
-constexpr uint32_t kCountMost = (1u << 20) - 1, kPrompt = 1u << 20, kSeen = kPrompt | kCountMost, kBiasMost = 2047;
-constexpr int kBiasShift = 21;
+// A table word of an entry: in its upper bits n - k for the first place k of
+// its bias in the row's list of n (0: none), as many bits as n has, below them
+// whether the prompt has it, then its count among the answer's tokens.  Rows
+// whose two lists are too long for that (2047 biases and 2^20 tokens, 16383
+// and 2^17) take two words an entry, and the run in two halves.
+struct Word {
+  uint32_t shift, prompt;
+  __device__ __forceinline__ explicit Word(uint32_t biases) : shift(min(31u, (uint32_t)__builtin_clz(biases | 1))), prompt(1u << (shift - 1)) {}
+  __device__ __forceinline__ uint32_t count(uint32_t w) const { return w & (prompt - 1); }
+  __device__ __forceinline__ uint32_t seen(uint32_t w) const { return w & (2 * prompt - 1); }
+  __device__ __forceinline__ uint32_t bias(uint32_t w) const { return w >> shift; }
+};
 constexpr uint32_t kLongPrompt = 0x80000000u;
 
 // A row's part of a list, as offsets within it that are in bounds whatever
@@ -132,14 +138,15 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
   const float presence = a.presence ? ld_const(a.presence + row) : 0.0f;
   const float frequency = a.frequency ? ld_const(a.frequency + row) : 0.0f;
 
+  const Word word(bias.n);
   auto penalize = [&](float v, bool seen, uint32_t count) {
     v *= !seen ? 1.0f : v > 0.0f ? inverse : repetition;
     return v - (count ? (float)count * frequency + presence : 0.0f);
   };
   auto value_at = [&](uint32_t i) { return i < THREADS ? first_values[i] : values[i]; };
   auto adjust = [&](float v, uint32_t w) {
-    v = penalize(v, w & kSeen, w & kCountMost);
-    if (w >> kBiasShift) v += value_at(kBiasMost - (w >> kBiasShift));
+    v = penalize(v, word.seen(w), word.count(w));
+    if (const uint32_t k = word.bias(w)) v += value_at(bias.n - k);
     return v;
   };
   // a unit, by its entries' words
@@ -150,11 +157,11 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) any |= w[e] = table[u * E + e];
 #pragma unroll
-    for (int e = 0; e < E; ++e) f[e] = penalize(f[e], w[e] & kSeen, w[e] & kCountMost);
-    if (any >> kBiasShift) {
+    for (int e = 0; e < E; ++e) f[e] = penalize(f[e], word.seen(w[e]), word.count(w[e]));
+    if (word.bias(any)) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (w[e] >> kBiasShift) f[e] += value_at(kBiasMost - (w[e] >> kBiasShift));
+        if (const uint32_t k = word.bias(w[e])) f[e] += value_at(bias.n - k);
     }
     return narrow_unit<DT, E>(f);
   };
@@ -197,7 +204,7 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
 
   if (!hist.n && !bias.n) {
     store();
-  } else if (hist.n <= kCountMost && bias.n <= kBiasMost) {
+  } else if (hist.n < word.prompt) {
     u32x4* cleared = reinterpret_cast<u32x4*>(table);
 #pragma unroll
     for (int i = 0; i < (int)(kRun / 4 / THREADS); ++i) cleared[i * THREADS + lane] = u32x4{0, 0, 0, 0};
@@ -205,9 +212,9 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
     for (uint32_t i0 = 0; i0 < bias.n;) {
       look(p, bias.n, i0, first, len, [&](uint32_t j, uint32_t i) {
         // the first place's bits, whatever else the word holds
-        const uint32_t bits = (kBiasMost - i) << kBiasShift;
-        for (uint32_t had = table[j]; had >> kBiasShift < bits >> kBiasShift;) {
-          const uint32_t now = atomicCAS(&table[j], had, bits | (had & kSeen));
+        const uint32_t bits = bias.n - i;
+        for (uint32_t had = table[j]; word.bias(had) < bits;) {
+          const uint32_t now = atomicCAS(&table[j], had, bits << word.shift | word.seen(had));
           if (now == had) break;
           had = now;
         }
@@ -216,7 +223,7 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
       ask(p, places, bias.n, i0);
     }
     first_values[lane] = value;
-    mark_tokens(t, first, len, kPrompt);
+    mark_tokens(t, first, len, word.prompt);
     __syncthreads();
     // Few units have an entry to adjust: a wave collects its own, and goes
     // over them at once.

@@ -130,6 +130,25 @@ def test_long_histories_and_lists(coll, longest, list_length, rows, dtype):
     assert all(torch.equal(a, b) for a, b in zip(out, zs))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("longest,list_length", [(131071, 16383), (131072, 16383), (65535, 16384), (65536, 16384), (1048576, 2047)])
+def test_one_row_of_a_long_history_and_a_long_list(coll, longest, list_length, dtype):
+    """Either side of what a word holds of both: one token all along, in the answer and in prompt and answer, and biased."""
+    import torch
+    g = rng(83, longest, list_length, dtype)
+    rows, v = 3, 2003
+    zs, ze = shards(g.normal(0, 3, (rows, v)), [0, 900, v], dtype, 0, 1)
+    c = Case(g, rows, v)
+    for r in (1, 2):
+        c.history[r] = np.full(longest, 17 + 1000 * (r == 2))
+        c.prompt[r] = r - 1
+        c.biases[r] = [(int(j), np.float32(b)) for j, b in zip(g.integers(0, v, list_length), g.normal(0, 5, list_length))]
+        c.biases[r][list_length - 1] = (1900 + r, np.float32(2.0))
+    out = [torch.full_like(z, float("nan")) for z in zs]
+    coll.coll_vocab_adjust(zs, out, **c.device())
+    check(out, *c.want(ze), dtype, "out")
+
+
 def test_edge_values(coll):
     """Masked entries and NaN, infinities, zeros of either sign and infinite biases."""
     import torch
