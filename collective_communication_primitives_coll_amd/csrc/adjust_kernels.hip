@@ -36,7 +36,8 @@ namespace {
 // its bias in the row's list of n (0: none), as many bits as n has, below them
 // whether the prompt has it, then its count among the answer's tokens.  Rows
 // whose two lists are too long for that (2047 biases and 2^20 tokens, 16383
-// and 2^17) take two words an entry, and the run in two halves.
+// and 2^17) take two words an entry, and the run in two halves: 85 us for the
+// 75 above with one such row (3740 biases, where they were 2047 at most).
 struct Word {
   uint32_t shift, prompt;
   __device__ __forceinline__ explicit Word(uint32_t biases) : shift(min(31u, (uint32_t)__builtin_clz(biases | 1))), prompt(1u << (shift - 1)) {}

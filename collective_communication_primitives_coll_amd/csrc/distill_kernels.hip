@@ -32,6 +32,12 @@
 // The loss is a small difference of what the two models have, and so is the
 // gradient's factor p_0 - q_0: what the join computes once a row (the
 // entries' exponentials and logarithms, all sums over them) is in 64 bits.
+//
+// 2048 x 131072 bf16 in 8 shards, 32 entries and a tail: 84-87 us for the
+// pieces (537 MB at 6.2-6.4 TB/s), 6 for the join, 168-174 for the gradient
+// (6.2-6.4 TB/s).  4 such rows of 20 entries: 9.4 us, of which the pieces take
+// 5.1 and the join 3.9, a wave's one chain of loads, sums and stores.
+// 777 x 50257 fp32 in 4 shards of odd widths, renormalised: 27, 5 and 53 us.
 #include "vocab_pieces.h"
 
 namespace coll {

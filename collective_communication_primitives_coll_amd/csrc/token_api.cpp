@@ -1,5 +1,6 @@
 // Host side of the token-wise operators' entry points: layer norm, RMS norm,
-// 8-bit checkpoints, vocabulary log probabilities.  Argument checks, byte ranges
+// 8-bit checkpoints, and over sharded logits log probabilities, distillation
+// and what a sampler adjusts.  Argument checks, byte ranges
 // and the record of the last HIP error are internal to coll_api.cpp, so that
 // file is part of this translation unit, and is not compiled by itself.
 #include "coll_api.cpp"

@@ -1,5 +1,6 @@
-// Device-side building blocks of the token-wise operators (layer norm,
-// 8-bit checkpoints, gated activation, vocabulary log probabilities).
+// Device-side building blocks of the token-wise operators (layer
+// norm, RMS norm, 8-bit checkpoints, gated activation, and what reads logits
+// over a sharded vocabulary).
 //
 // A row of `hidden` elements is cut into units of 16 bytes, 8 elements of
 // bf16 or 4 of fp32, one to a lane: the lanes of a wave then load and store

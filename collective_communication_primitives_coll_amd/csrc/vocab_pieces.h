@@ -1,5 +1,6 @@
 // Rows of a vocabulary that lies in p shards, cut into pieces of one wave each:
-// what the kernels over sharded logits share (log probabilities, distillation).
+// what the kernels over sharded logits share (log probabilities,
+// distillation, and of the small parts a sampler's adjustments).
 #pragma once
 
 #include <float.h>
