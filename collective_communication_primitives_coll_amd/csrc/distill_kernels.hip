@@ -239,22 +239,27 @@ __global__ __launch_bounds__(kBlock) void distill_join_kernel(DistillJoinArgs a)
     const float zi = as_global(a.zs)[at];  // (not written where the entry is in no shard)
     z[k] = ok ? zi : -inf;
   }
-  // an index's first entry counts
-  bool again[NT] = {};
+  // An index's first entry counts: later ones' lanes as bits, eight entries at
+  // a time to compare with (those past the last have no index, and nothing to
+  // lose).
+  uint64_t again[NT] = {};
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int most = min(a.top - j * kWave, kWave);
-    for (int b = 0; b < most; ++b) {
-      const int32_t other = __builtin_amdgcn_readlane(id[j], b);
+    for (int b0 = 0; b0 < most; b0 += 8) {
 #pragma unroll
-      for (int k = j; k < NT; ++k) again[k] = again[k] || (id[k] == other && (k > j || lane > b));
+      for (int b = b0; b < b0 + 8; ++b) {
+        const int32_t other = __builtin_amdgcn_readlane(id[j], b);
+#pragma unroll
+        for (int k = j; k < NT; ++k) again[k] |= __ballot(id[k] == other) & (k > j ? ~0ull : ~1ull << b);
+      }
     }
   }
   bool counts[NT];
   bool any = false;
 #pragma unroll
   for (int k = 0; k < NT; ++k) {
-    counts[k] = id[k] >= 0 && !again[k] && (a.tail || l[k] != -inf);
+    counts[k] = id[k] >= 0 && !(again[k] >> lane & 1) && (a.tail || l[k] != -inf);
     any = any || counts[k];
   }
   any = __any(any);
