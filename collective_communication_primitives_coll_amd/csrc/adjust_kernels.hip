@@ -10,9 +10,9 @@
 // row's shard.  It asks for the run's logits, which stay in registers, and
 // marks the row's history and biases in a table of the run's entries in LDS
 // while they come.  Every workgroup of a row goes over the whole history and
-// keeps what falls into its run: the longer the run the less often, so runs
-// are as long as two workgroups' tables to a CU allow, and a row's runs follow
-// each other on one XCD, whose L2 then serves the history to all but the
+// keeps what falls into its run: the longer the run the less often, and the
+// fewer workgroups share a CU (two of 2048 units, five of 1024).  A row's runs
+// follow each other on one XCD, whose L2 then serves the history to all but the
 // first.  Few units have a mark: a wave collects its own from its lanes and
 // adjusts them at once, before the mask, which needs no arithmetic.
 // 512 x 131072 bf16 in 8 shards, masks, 100 biases and histories of 4000
@@ -20,9 +20,10 @@
 // 4000 in every row, 61 without masks and biases, 48 with nothing to mark
 // (5.6 TB/s): what marks cost is the instructions of going over the history
 // and of the units to adjust (570 a wave, 330 without masks and biases), not
-// waiting: asking for the next tokens while these are looked at changed nothing.  Runs of 8192 entries took 73 for 67, and 82 where a row's runs
-// went to all XCDs; every lane adjusting its own units 85.  Where few rows
-// leave CUs without work, runs are short: 4 rows of 131072, 400 tokens: 5.4 us.
+// waiting: asking for the next tokens while these are looked at changed
+// nothing.  82 where a row's runs went to all XCDs, 85 with every lane adjusting
+// its own units.  4 rows of 131072, 400 tokens: 5.3 us; 333 x 50257 fp32 in 4
+// shards, 1500 tokens: 33 us.
 //
 // Counts are whole numbers and a bias's first entry wins by its place in the
 // list, so results do not depend on the order of the atomics.
@@ -206,9 +207,10 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
   if (!hist.n && !bias.n) {
     store();
   } else if (hist.n < word.prompt) {
-    u32x4* cleared = reinterpret_cast<u32x4*>(table);
+    u32x4* cleared = reinterpret_cast<u32x4*>(table);  // as far as the run goes, at least
 #pragma unroll
-    for (int i = 0; i < (int)(kRun / 4 / THREADS); ++i) cleared[i * THREADS + lane] = u32x4{0, 0, 0, 0};
+    for (int i = 0; i < (int)(kRun / 4 / THREADS); ++i)
+      if ((uint32_t)i * THREADS * 4 < len) cleared[i * THREADS + lane] = u32x4{0, 0, 0, 0};
     __syncthreads();
     for (uint32_t i0 = 0; i0 < bias.n;) {
       look(p, bias.n, i0, first, len, [&](uint32_t j, uint32_t i) {
@@ -234,8 +236,11 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
       uint32_t any = 0;
+      // (behind the run's end the table is not cleared)
+      if (i * THREADS + lane < full) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) any |= table[(i * THREADS + lane) * E + e];
+        for (int e = 0; e < E; ++e) any |= table[(i * THREADS + lane) * E + e];
+      }
       hit[i] = any != 0;
       const unsigned long long m = __ballot(hit[i]);
       place[i] = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
@@ -298,12 +303,6 @@ __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
   }
 }
 
-// Runs of 2048 units where that still makes some 128 workgroups, else of 256:
-// bf16 rows of 131072 in 8 shards and histories of 4000, long and short runs:
-// 4 rows 9.0 and 7.1 us, 16 rows 8.7 and 9.7, 32 rows 9.0 and 15.0; 16 rows of
-// 50256 in 4 shards (64 long runs) 8.2 and 7.8.
-constexpr uint64_t kManyRuns = 128;
-
 // Workgroups go to the XCDs in turn: with enough rows the runs of one are kept
 // on one XCD, whose L2 then serves the row's history to all but the first.
 constexpr int kXcds = 8;
@@ -329,12 +328,33 @@ int adjust_t(AdjustArgs a, hipStream_t s) {
   return 0;
 }
 
+// Runs: short ones where few rows leave CUs without work; else no longer than
+// the shards are, since a workgroup's lanes without entries and its table
+// keep others out; and the longest where long histories are gone over once a
+// run.  us of runs of 256 units (256 lanes, and 128 of two units each), 1024
+// (256 lanes) and 2048 (512 lanes), bf16, masks and biases, by shards and tokens:
+//   64 rows of 8 x 4096, 1000 tokens          6.9   6.8    6.9    8.2
+//   480 rows of 8 x 526, none                16.3  12.0   21.8   39.6
+//   1024 rows of 5 x 3319, 1000              40.8  31.0   34.1   58.1
+//   512 rows of 8 x 8192, 1000               57.7  41.7   31.9   48.3
+//   512 rows of 8 x 16384, none             100.3  68.0   51.3   56.6
+//   the same, 4000 (20000) in every row     140.2 125.1   65.1 (135) 65.0 (109)
+//   the same, 4000 on average, some 50000       -   169   87.1   80.0
+constexpr uint64_t kManyRuns = 512, kLongHistory = 2000;
+
 template <int DT>
 int adjust_d(const AdjustArgs& a, hipStream_t s) {
-  constexpr uint64_t kLong = 2048 * kElems<DT>;
-  uint64_t runs = 0;
-  for (int r = 0; r < a.p; ++r) runs += ((uint64_t)(a.first_index[r + 1] - a.first_index[r]) + kLong - 1) / kLong;
-  return a.rows >= (kManyRuns + runs - 1) / runs ? adjust_t<DT, 512, 4>(a, s) : adjust_t<DT, 256, 1>(a, s);
+  constexpr int E = kElems<DT>;
+  int64_t runs = 0, longest = 0;
+  for (int r = 0; r < a.p; ++r) {
+    const int64_t n = a.first_index[r + 1] - a.first_index[r];
+    runs += (n + 1024 * E - 1) / (1024 * E);
+    longest = std::max(longest, n);
+  }
+  if (a.rows < (kManyRuns + (uint64_t)runs - 1) / (uint64_t)runs) return adjust_t<DT, 256, 1>(a, s);
+  if (longest <= 256 * E) return adjust_t<DT, 128, 2>(a, s);
+  if (longest <= 1024 * E || a.ntokens / a.rows < kLongHistory) return adjust_t<DT, 256, 4>(a, s);
+  return adjust_t<DT, 512, 4>(a, s);
 }
 
 }  // namespace

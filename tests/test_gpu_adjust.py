@@ -149,6 +149,25 @@ def test_one_row_of_a_long_history_and_a_long_list(coll, longest, list_length, d
     check(out, *c.want(ze), dtype, "out")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("widths", [(526, 2048, 1), (2047, 1030, 0, 9), (2049, 8192, 3), (4100, 8191), (8193, 700), (16384, 16385, 5)])
+def test_shards_and_the_lengths_of_runs(coll, widths, dtype):
+    """Shards that end with a run of each length, before or behind one."""
+    import torch
+    g = rng(84, len(widths), widths[0], dtype)
+    widths = [w if dtype == BF16 else w // 2 + w % 2 for w in widths]
+    rows, cuts = 140, np.cumsum([0, *widths])
+    v = int(cuts[-1])
+    zs, ze = shards(g.normal(0, 3, (rows, v)), list(cuts), dtype, 3, 1)
+    c = Case(g, rows, v, lengths=(0, 1, 30, 600))
+    for r in range(0, rows, 2):                               # every run's last entries
+        c.history[r] = np.concatenate([c.history[r], cuts[1:] - 1])
+        c.biases[r] = c.biases[r] + [(int(x) - 1, np.float32(3.0)) for x in cuts[1:]]
+    out = [torch.full_like(z, float("nan")) for z in zs]
+    coll.coll_vocab_adjust(zs, out, **c.device())
+    check(out, *c.want(ze), dtype, "out")
+
+
 def test_edge_values(coll):
     """Masked entries and NaN, infinities, zeros of either sign and infinite biases."""
     import torch
