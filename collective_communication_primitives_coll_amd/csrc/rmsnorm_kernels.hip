@@ -68,9 +68,8 @@ constexpr int rows_of() {
   return (RES ? TPR >= (DT == kF32 ? 192 : 256) : TPR >= 512 && !FP8) ? 1 : 2;
 }
 
-template <int DT, int WT, int TPR, int NU, bool TAIL, bool RES, bool FP8>
+template <int DT, int WT, int TPR, int NU, bool TAIL, bool RES, bool FP8, int E = kElems<DT>>
 __global__ __launch_bounds__(block_of(TPR)) void rms_forward_kernel(RmsArgs a) {
-  constexpr int E = kElems<DT>;
   constexpr int kRows = rows_of<DT, TPR, RES, FP8>();
   __shared__ float red[2][kRows][waves_of(TPR)];
   const int rank = blockIdx.y;
@@ -481,18 +480,19 @@ __global__ __launch_bounds__(1024) void rms_backward_wide_rows_kernel(RmsArgs a)
   }
 }
 
-// The kernel that takes rows of a width: lanes to a row and units to a lane
-// (0: the wide ones).  Codes want a group's lanes in one run of a row's, at
-// most a wave: rows of 16 lanes take 64 for wider groups, and fp32 rows of
-// groups of 512 the wide kernel, whose lanes hold 8 elements in every type.
+// The kernel that takes rows of a width: lanes to a row and units of 8 elements
+// to a lane (0: the wide ones).  Codes want a group's lanes in one run of a
+// row's, at most a wave: rows of 16 lanes take 64 for wider groups, and fp32
+// rows of groups of 512 have 8 elements to a lane (5 x 11770 x 512: 30 us, and
+// 468 in the wide kernel).
+constexpr uint64_t kLanesGroup4 = 4 * kWave;  // widest group of lanes with 4 elements
 void rms_shape(int dtype, uint64_t hidden, uint64_t group, int* tpr, int* nu) {
   row_shape(hidden, tpr, nu);
-  const uint64_t elems = dtype == kF32 ? 4 : 8;
+  const uint64_t elems = dtype == kF32 && group <= kLanesGroup4 ? 4 : 8;
   if (*tpr == 16 && group > 16 * elems) {
     *tpr = 64;
     *nu = 1;
   }
-  if (group > kWave * elems) *tpr = 0;
 }
 
 // The forward pass's arguments n rows on.
@@ -510,7 +510,8 @@ void skip_rows(RmsArgs& a, uint64_t n, uint64_t row_bytes) {
 template <int DT, int WT, bool RES, bool FP8>
 int forward_t(const RmsArgs& a, hipStream_t s) {
   int tpr, nu;
-  rms_shape(DT, a.hidden, FP8 ? uint64_t{1} << a.glog : 0, &tpr, &nu);
+  const uint64_t group = FP8 ? uint64_t{1} << a.glog : 0;
+  rms_shape(DT, a.hidden, group, &tpr, &nu);
   if (!tpr) {
     const dim3 grid((uint32_t)std::min<uint64_t>(a.rows, 65536), a.ranks);
     hipLaunchKernelGGL((rms_forward_wide_kernel<DT, WT, RES, FP8>), grid, dim3(1024), 0, s, a);
@@ -528,7 +529,12 @@ int forward_t(const RmsArgs& a, hipStream_t s) {
       left -= part.rows;
       const dim3 grid((uint32_t)((part.rows + run - 1) / run), a.ranks);
       if constexpr (FP8) {  // whole groups, so whole units
-        hipLaunchKernelGGL((rms_forward_kernel<DT, WT, TPR, NU, PACKED, RES, true>), grid, block, 0, s, part);
+        if constexpr (DT == kF32 && !PACKED) {
+          if (group > kLanesGroup4) hipLaunchKernelGGL((rms_forward_kernel<DT, WT, TPR, NU / 2, false, RES, true, 8>), grid, block, 0, s, part);
+          else hipLaunchKernelGGL((rms_forward_kernel<DT, WT, TPR, NU, false, RES, true>), grid, block, 0, s, part);
+        } else {
+          hipLaunchKernelGGL((rms_forward_kernel<DT, WT, TPR, NU, PACKED, RES, true>), grid, block, 0, s, part);
+        }
       } else {
         if (PACKED || a.hidden % kElems<DT>) hipLaunchKernelGGL((rms_forward_kernel<DT, WT, TPR, NU, true, RES, false>), grid, block, 0, s, part);
         else hipLaunchKernelGGL((rms_forward_kernel<DT, WT, TPR, NU, PACKED, RES, false>), grid, block, 0, s, part);
