@@ -328,19 +328,25 @@ int adjust_t(AdjustArgs a, hipStream_t s) {
   return 0;
 }
 
-// Runs: short ones where few rows leave CUs without work; else no longer than
-// the shards are, since a workgroup's lanes without entries and its table
-// keep others out; and the longest where long histories are gone over once a
-// run.  us of runs of 256 units (256 lanes, and 128 of two units each), 1024
-// (256 lanes) and 2048 (512 lanes), bf16, masks and biases, by shards and tokens:
-//   64 rows of 8 x 4096, 1000 tokens          6.9   6.8    6.9    8.2
-//   480 rows of 8 x 526, none                16.3  12.0   21.8   39.6
-//   1024 rows of 5 x 3319, 1000              40.8  31.0   34.1   58.1
-//   512 rows of 8 x 8192, 1000               57.7  41.7   31.9   48.3
-//   512 rows of 8 x 16384, none             100.3  68.0   51.3   56.6
-//   the same, 4000 (20000) in every row     140.2 125.1   65.1 (135) 65.0 (109)
-//   the same, 4000 on average, some 50000       -   169   87.1   80.0
-constexpr uint64_t kManyRuns = 512, kLongHistory = 2000;
+// Runs: of one unit to a lane where few rows leave CUs without work; else of 1024
+// units to 256 lanes, but where shards are shorter of 256 units to 128,
+// since a workgroup's lanes without entries and its table keep others out.
+// Long histories want the longest runs, which go over them the least often,
+// and more lanes.  us with runs of 256 units (256 lanes, and 128), 512, 1024 and
+// 2048 (512 lanes), bf16, masks and biases, by shards and tokens (~: on average,
+// most less, some ten times as many):
+//   4 rows of 8 x 16384, 400 tokens           5.4     -   5.5
+//   the same, 20000 tokens                   11.9     -  10.1  13.7  12.2
+//   16 rows of 8 x 16384, ~4000              12.1     -   9.9  13.6  11.3
+//   64 rows of 8 x 4096, ~400 (~20000)        6.9     -   7.5   7.1 (56)  8.6 (35)
+//   480 rows of 8 x 526, none                16.3  12.0  33.2  21.8  39.6
+//   266 rows of 16 x 412, ~5700              38.4  51.6  47.7  43.5  57.5
+//   1024 rows of 5 x 3319, 1000              40.8  31.0  49.6  34.1  58.1
+//   512 rows of 8 x 8192, 1000               57.7  41.7  72.4  31.9  48.3
+//   512 rows of 8 x 16384, none             100.3  68.0   124  51.3  56.6
+//   the same, 4000 (20000)                  140.2 125.1   146  65.1 (135)  65.0 (109)
+//   the same, ~4000                             -   169   174  87.1  80.0
+constexpr uint64_t kFewRuns = 512, kManyRuns = 1024, kLongHistory = 2000;
 
 template <int DT>
 int adjust_d(const AdjustArgs& a, hipStream_t s) {
@@ -351,10 +357,12 @@ int adjust_d(const AdjustArgs& a, hipStream_t s) {
     runs += (n + 1024 * E - 1) / (1024 * E);
     longest = std::max(longest, n);
   }
-  if (a.rows < (kManyRuns + (uint64_t)runs - 1) / (uint64_t)runs) return adjust_t<DT, 256, 1>(a, s);
-  if (longest <= 256 * E) return adjust_t<DT, 128, 2>(a, s);
-  if (longest <= 1024 * E || a.ntokens / a.rows < kLongHistory) return adjust_t<DT, 256, 4>(a, s);
-  return adjust_t<DT, 512, 4>(a, s);
+  auto fewer = [&](uint64_t than) { return a.rows < (than + (uint64_t)runs - 1) / (uint64_t)runs; };
+  const bool history = a.ntokens / a.rows >= kLongHistory;
+  if (fewer(kFewRuns)) return history ? adjust_t<DT, 512, 1>(a, s) : adjust_t<DT, 256, 1>(a, s);
+  if (history && (longest > 1024 * E || fewer(kManyRuns))) return adjust_t<DT, 512, 4>(a, s);
+  if (!history && longest <= 256 * E) return adjust_t<DT, 128, 2>(a, s);
+  return adjust_t<DT, 256, 4>(a, s);
 }
 
 }  // namespace
