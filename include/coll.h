@@ -423,9 +423,9 @@ coll_status_t coll_allreduce_batch_noalloc(const coll_call_t* calls, int ncalls,
                                            void* stream);
 
 /* ===========================================================================
- * Token-wise operators of a training step
+ * Token-wise operators of a training or serving step
  *
- * What a data- or tensor-parallel training step computes between its
+ * What a data- or tensor-parallel step computes between its
  * collectives and its matrix products, over the same p logical ranks and
  * under the same contract: host arrays of p device pointers, everything
  * validated before anything is enqueued, nothing allocated (the caller
