@@ -23,7 +23,7 @@
 // waiting: asking for the next tokens while these are looked at changed
 // nothing.  82 where a row's runs went to all XCDs, 85 with every lane adjusting
 // its own units.  4 rows of 131072, 400 tokens: 5.3 us; 333 x 50257 fp32 in 4
-// shards, 1500 tokens: 33 us.
+// shards, 1500 tokens: 32 us.
 //
 // Counts are whole numbers and a bias's first entry wins by its place in the
 // list, so results do not depend on the order of the atomics.
@@ -62,13 +62,17 @@ struct Span {
   }
 };
 
-// Tokens that a lane asks for at a time.
-constexpr int kTokensAhead = 8;
+// Tokens that a lane asks for at a time: with four, 24 registers fewer let one
+// more workgroup share a CU, where its table does (333 x 50256 fp32: 32 us for
+// 34; 512 x 65536 bf16, 1000 tokens: 31.5 for 32.8; with 20000 82 for 77).
+template <int THREADS, int UNITS>
+constexpr int kAhead = THREADS < 512 && UNITS > 1 ? 4 : 8;
 
 template <int DT, int THREADS, int UNITS>
 __global__ __launch_bounds__(THREADS) void adjust_kernel(AdjustArgs a) {
   constexpr int B = Traits<DT>::B, E = kElems<DT>;
   constexpr uint32_t kRun = UNITS * THREADS * E;
+  constexpr int kTokensAhead = kAhead<THREADS, UNITS>;
   using S = typename Traits<DT>::S;
   __shared__ __attribute__((aligned(16))) uint32_t table[kRun];
   __shared__ u32x4 held[THREADS];           // a wave's units to adjust
