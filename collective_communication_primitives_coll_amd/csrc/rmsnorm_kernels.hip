@@ -268,11 +268,19 @@ struct DxRow {
   }
 };
 
+// Sum over a wave's four rows of 16 lanes, on every lane.
+__device__ __forceinline__ float rows_sum(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 template <int DT, int WT, int TPR, int NU, bool TAIL, bool DH>
 __global__ __launch_bounds__(block_of(TPR)) void rms_backward_kernel(RmsArgs a) {
   constexpr int E = kElems<DT>, RPB = block_of(TPR) / TPR, AHEAD = kAhead<TPR>;
   __shared__ float red[2][1][waves_of(TPR)];
-  __shared__ float fold[RPB > 1 ? NU * E * TPR : 1];
+  __shared__ float fold[RPB > 1 ? kBlock / kWave : 1][RPB > 1 ? NU * E * TPR : 1];
   const uint32_t lane = threadIdx.x % TPR, H = (uint32_t)a.hidden;
   const uint64_t row_bytes = (uint64_t)H * Traits<DT>::B;
   const uint64_t stride = (uint64_t)gridDim.x * RPB;
@@ -383,22 +391,25 @@ __global__ __launch_bounds__(block_of(TPR)) void rms_backward_kernel(RmsArgs a) 
   }
   float* ws = a.ws + (uint64_t)blockIdx.x * H;
   if constexpr (RPB > 1) {
-    // the workgroup's groups of lanes add their sums in turn
-    const int mine = (int)own_row<TPR>(0);
-    for (int k = 0; k < RPB; ++k) {
-      if (mine == k) {
+    // a wave's groups of lanes add their sums, then the first group those of
+    // the workgroup's waves, in their order (one group after the other: 8 x
+    // 500 x 256 bf16 15.0 us for 13.1)
+    const uint32_t mine = threadIdx.x / TPR, wave = threadIdx.x / kWave;
 #pragma unroll
-        for (int i = 0; i < NU; ++i)
+    for (int i = 0; i < NU; ++i)
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            float* to = fold + (i * E + e) * TPR + lane;
-            dg[i][e] += k ? to[0] : 0.0f;
-            to[0] = dg[i][e];
-          }
+      for (int e = 0; e < E; ++e) {
+        if constexpr (TPR < kWave) dg[i][e] = rows_sum(dg[i][e]);
+        if (mine % (RPB * kWave / kBlock) == 0) fold[wave][(i * E + e) * TPR + lane] = dg[i][e];
       }
-      __syncthreads();
-    }
-    if (mine != RPB - 1) return;
+    __syncthreads();
+    if (mine) return;
+#pragma unroll
+    for (int i = 0; i < NU; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int k = 1; k < kBlock / kWave; ++k) dg[i][e] += fold[k][(i * E + e) * TPR + lane];
   }
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
