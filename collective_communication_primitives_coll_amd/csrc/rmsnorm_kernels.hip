@@ -34,10 +34,21 @@ constexpr float kMost = 0x1p120f, kLeast = 0x1p-90f, kDown = 0x1p-80f, kUp = 0x1
 __device__ __forceinline__ float square_scale(float q, float eps) {
   return !(q < kMost) ? kDown : q < kLeast && eps < kEpsLeast ? kUp : 1.0f;
 }
-// 1 / sqrt(mean h^2 + eps) from the sum of (h k)^2.
-__device__ __forceinline__ float rstd_of(float q, float k, float hidden, float eps) {
-  return rsqrtf(q / hidden + eps * k * k) * k;
-}
+// 1 / sqrt(mean h^2 + eps) from the sum of (h k)^2, as the product of two
+// factors: the root of the scaled sum, and k.  Their product may leave fp32's
+// range where values times it do not (rows below 2^-128, whose values are all
+// denormal), so a value takes one after the other, in the order that stays in
+// range: by 2^100 before the root, by 2^-80 after it.  1 is exact either way.
+struct Rstd {
+  float first, second;
+  __device__ __forceinline__ Rstd(float q, float k, float hidden, float eps) {
+    const float root = rsqrtf(q / hidden + eps * k * k);
+    first = k > 1.0f ? k : root;
+    second = k > 1.0f ? root : k;
+  }
+  __device__ __forceinline__ float times(float v) const { return v * first * second; }
+  __device__ __forceinline__ float value() const { return first * second; }
+};
 
 template <int DT, int E>
 __device__ __forceinline__ RawUnit<DT, E> add_units(const RawUnit<DT, E>& a, const RawUnit<DT, E>& b) {
@@ -134,7 +145,7 @@ __global__ __launch_bounds__(block_of(TPR)) void rms_forward_kernel(RmsArgs a) {
   for (int k = 0; k < kRows; ++k) {
     const uint64_t row = row0 + k;
     if (row >= a.rows) break;
-    const float rstd = rstd_of(q[k], by[k], (float)H, a.eps);
+    const Rstd rstd(q[k], by[k], (float)H, a.eps);
     if (RES && a.h[rank]) {
       const Row<DT, E, TAIL> h(static_cast<uint8_t*>(a.h[rank]) + row * row_bytes, H);
 #pragma unroll
@@ -151,7 +162,7 @@ __global__ __launch_bounds__(block_of(TPR)) void rms_forward_kernel(RmsArgs a) {
       widen_unit(raw[k][i], f);
       widen_unit(gamma[i], g);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = f[e] * rstd * g[e];
+      for (int e = 0; e < E; ++e) f[e] = rstd.times(f[e]) * g[e];
       if (plain) y.template put<true>(i * TPR + lane, narrow_unit<DT, E>(f));
       if constexpr (FP8) {
         const uint32_t u = i * TPR + lane;
@@ -161,7 +172,7 @@ __global__ __launch_bounds__(block_of(TPR)) void rms_forward_kernel(RmsArgs a) {
       }
     }
     if constexpr (FP8 && TPR >= kWave) pad_codes(y8, H, a.row_bytes, a.glog, lane);
-    if (lane == 0 && a.rstd[rank]) as_global(a.rstd[rank])[row] = rstd;
+    if (lane == 0 && a.rstd[rank]) as_global(a.rstd[rank])[row] = rstd.value();
   }
 }
 
@@ -218,21 +229,21 @@ __global__ __launch_bounds__(1024) void rms_forward_wide_kernel(RmsArgs a) {
     float s[1] = {q[0]};
     if (by != 1.0f) row_sums<TPR, 1>(s, red[1]);
     else __syncthreads();
-    const float rstd = rstd_of(s[0], by, (float)H, a.eps);
+    const Rstd rstd(s[0], by, (float)H, a.eps);
     for (uint64_t k = 0; k < steps; ++k) {
       const uint64_t u = k * TPR + threadIdx.x;
       unit(u, true);
       float g[8];
       weight_unit<WT>(a.gamma[rank], 1.0f, u, full, part, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
+      for (int e = 0; e < 8; ++e) f[e] = rstd.times(f[e]) * g[e];
       if (y) put_unit<DT>(y, u, full, part, f);
       if constexpr (FP8) {
         const RawUnit<kE4M3, 8> code = encode_values<8>(f, a.glog);
         if (u < full) store_codes<8, true>(y8, H, a.row_bytes, u * 8, a.glog, code);
       }
     }
-    if (threadIdx.x == 0 && a.rstd[rank]) as_global(a.rstd[rank])[row] = rstd;
+    if (threadIdx.x == 0 && a.rstd[rank]) as_global(a.rstd[rank])[row] = rstd.value();
   }
 }
 

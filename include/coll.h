@@ -477,8 +477,11 @@ size_t coll_layernorm_workspace_bytes(int p, size_t rows, size_t hidden);
  * elements of dtype.  gamma[r]: rank r's copy of the weights, `hidden`
  * elements of wdtype (COLL_F32, or dtype); optional (ones).  rstd[r]: fp32
  * [rows], s for the backward pass; optional.  Statistics are those of the
- * rounded h, whether it is stored or not, and hold over the whole range of
- * fp32 values.  A row of zeros with eps = 0 gives NaN.
+ * rounded h, whether it is stored or not, and y holds over the whole range of
+ * fp32 values.  Where s leaves fp32 (a root mean square below 2^-128, eps
+ * next to nothing), rstd is +infinity, with which the backward pass gives no
+ * finite gradient of that row, nor of gamma.  A row of zeros with eps = 0
+ * gives NaN.
  * In place: h[r] and y[r] may each be x[r] or residual[r] (not both the
  * same).  1 <= hidden < 2^31; rows == 0 is a no-op. */
 coll_status_t coll_rmsnorm(const void* const* x, const void* const* residual, const void* const* gamma,

@@ -232,6 +232,47 @@ def test_output_in_8_bits(coll, p, rows, hidden, group, dtype, wdtype):
             assert np.array_equal(rows8, token_ops.ckpt8_rows(y[r].cpu().numpy(), group))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("hidden", [7, 48, 100, 512, 1024, 2049, 5120, 7168, 16384, 20003, 20480])
+def test_rows_whose_reciprocal_leaves_fp32(coll, hidden, residual, dtype):
+    """1 / rms above the largest fp32 value, or among its denormals: y and its 8-bit rows are those of any other row;
+    rstd is the nearest fp32 value, an infinity above them."""
+    import torch
+    g = rng(58, hidden, residual, dtype)
+    down = [-129, -130, -131] if dtype == BF16 else [-129, -130, -140, -147]
+    scale = 2.0 ** np.array([*down, 0, -127, 126, *down, 20])
+    rows = len(scale)
+    sign = np.where(g.random((rows, hidden)) < 0.5, -1, 1)
+    x, xe = dev(g.uniform(0.5, 1.5, (rows, hidden)) * sign * scale[:, None], dtype)
+    if residual:                                              # the values from both: x again, or nothing
+        res, he = [x], 2 * xe
+        he[5], res[0] = xe[5], x.clone()
+        res[0][5] = 0.0
+    else:
+        res, he = None, xe
+    gamma, ge = dev(g.normal(1, 0.2, hidden), F32)
+    y, rstd, h = new((rows, hidden), dtype), f32(rows), [new((rows, hidden), dtype)] if residual else None
+    coll.coll_rmsnorm([x], [gamma], [y], hidden, eps=0.0, residual=res, h=h, rstd=[rstd])
+    if residual:
+        close(host(h[0]), he, 0.0, "h")
+    ye, re = token_ops.rmsnorm(he, ge, 0.0)
+    over = re > 2.0 ** 128
+    assert over.any() and np.isposinf(host(rstd)[over]).all()
+    close(host(rstd)[~over], re[~over], re[~over] * (chain(hidden) / 2 + 8) * U + 2.0 ** -149, "rstd")
+    close(host(y), ye, y_tol(ye, hidden, dtype), "y")
+    if hidden % 16 == 0:
+        group = 512 if hidden % 512 == 0 else 16
+        rb = coll.coll_ckpt8_row_bytes(hidden, group)
+        y8, again = u8(rows, rb), new((rows, hidden), dtype)
+        coll.coll_rmsnorm_fp8([x], [gamma], [y8], hidden, group, eps=0.0, residual=res, y=[again])
+        close(host(again), ye, y_tol(ye, hidden, dtype), "y beside the codes")
+        value = token_ops.ckpt8_values(y8.cpu().numpy(), hidden, group).astype(np.float64)
+        amax = np.repeat(np.abs(ye).reshape(rows, -1, group).max(2), group, axis=1)
+        # half a step of e4m3 (or of its subnormals, 2^-10 of the scale amax / 448), off by roundings far below 2^-12
+        close(value, ye, (2.0 ** -4 * np.abs(ye) + 2.0 ** -10 * amax / 448) * (1 + 2.0 ** -12) + 2 * y_tol(ye, hidden, F32), "values")
+
+
 def test_codes_of_rows_with_a_non_finite_value(coll):
     for hidden, dtype in ((64, F32), (2560, BF16), (20480, BF16)):
         x = rng(54).normal(0, 1, (3, hidden))
