@@ -273,6 +273,41 @@ def test_rows_whose_reciprocal_leaves_fp32(coll, hidden, residual, dtype):
         close(value, ye, (2.0 ** -4 * np.abs(ye) + 2.0 ** -10 * amax / 448) * (1 + 2.0 ** -12) + 2 * y_tol(ye, hidden, F32), "values")
 
 
+@pytest.mark.parametrize("dtype,hidden,group", [(BF16, 64, 16), (F32, 256, 256), (BF16, 512, 512), (F32, 2560, 64), (BF16, 7168, 128), (F32, 7168, 512),
+                                                (BF16, 16384, 128), (BF16, 20480, 512)])
+def test_in_place_forms_with_8_bit_rows(coll, dtype, hidden, group):
+    """h and y in the place of x and the residual, either of them or both, in the pass that writes the codes."""
+    import torch
+    g = rng(59, hidden, group, dtype)
+    p, rows = 2, 5
+    x, res = [T([dev(g.normal(0, 1, (rows, hidden)), dtype) for _ in range(p)]) for _ in range(2)]
+    gamma = [dev(g.normal(1, 0.2, hidden), F32)[0]] * p
+    rb = coll.coll_ckpt8_row_bytes(hidden, group)
+
+    def run(hx, yx, x=x, res=res):
+        at = {"x": [t.clone() for t in x], "res": [t.clone() for t in res] if res else None, "new": [new((rows, hidden), dtype) for _ in range(p)], None: None}
+        y8, rstd = u8(p, rows, rb), f32(p, rows)
+        if "new" == hx == yx:
+            at["new2"] = [new((rows, hidden), dtype) for _ in range(p)]
+            yx = "new2"
+        coll.coll_rmsnorm_fp8(at["x"], gamma, list(y8), hidden, group, residual=at["res"], h=at[hx], rstd=list(rstd), y=at[yx])
+        return at[hx], at[yx], y8, rstd
+    h, y, y8, rstd = run("new", "new")
+    for hx in ("x", "res", "new", None):
+        for yx in ("x", "res", "new", None):
+            if hx == yx:
+                continue
+            got = run(hx, yx)
+            assert hx is None or all(torch.equal(a, b) for a, b in zip(h, got[0])), (hx, yx)
+            assert yx is None or all(torch.equal(a, b) for a, b in zip(y, got[1])), (hx, yx)
+            assert torch.equal(y8, got[2]) and torch.equal(rstd, got[3]), (hx, yx)
+    plain = run(None, "new", res=None)
+    for yx in ("x", None):
+        got = run(None, yx, res=None)
+        assert yx is None or all(torch.equal(a, b) for a, b in zip(plain[1], got[1]))
+        assert torch.equal(plain[2], got[2]) and torch.equal(plain[3], got[3])
+
+
 def test_codes_of_rows_with_a_non_finite_value(coll):
     for hidden, dtype in ((64, F32), (2560, BF16), (20480, BF16)):
         x = rng(54).normal(0, 1, (3, hidden))
