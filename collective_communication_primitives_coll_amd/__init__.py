@@ -1141,7 +1141,8 @@ def coll_vocab_adjust(logits, out, tokens=None, offsets=None, prompt=None, repet
                       defer: bool = False):
     """Penalties, biases and masks on the shards logits[r] [rows, vocab_r],
     written to out[r] (the same tensors: in place).  tokens int64 with offsets
-    int64 [rows + 1] and (or None) prompt int64 [rows]: the rows' histories;
+    int64 [rows + 1] and (or None) prompt int64 [rows]: the rows' histories
+    (ntokens: how many of a longer buffer the offsets can reach);
     repetition, presence and frequency (or None) fp32 [rows]; bias_idx int64 and
     bias fp32 with bias_offsets int64 [rows + 1]; mask int32 or uint32
     [rows, words], bit j % 32 of word j // 32 for entry j, 1: allowed."""

@@ -11,19 +11,21 @@
 // marks the row's history and biases in a table of the run's entries in LDS
 // while they come.  Every workgroup of a row goes over the whole history and
 // keeps what falls into its run: the longer the run the less often, and the
-// fewer workgroups share a CU (two of 2048 units, five of 1024).  A row's runs
-// follow each other on one XCD, whose L2 then serves the history to all but the
-// first.  Few units have a mark: a wave collects its own from its lanes and
-// adjusts them at once, before the mask, which needs no arithmetic.
-// 512 x 131072 bf16 in 8 shards, masks, 100 biases and histories of 4000
-// tokens on average (most shorter, some of 30000 and more): 69-75 us; 67 with
-// 4000 in every row, 61 without masks and biases, 48 with nothing to mark
-// (5.6 TB/s): what marks cost is the instructions of going over the history
-// and of the units to adjust (570 a wave, 330 without masks and biases), not
-// waiting: asking for the next tokens while these are looked at changed
-// nothing.  82 where a row's runs went to all XCDs, 85 with every lane adjusting
-// its own units.  4 rows of 131072, 400 tokens: 5.3 us; 333 x 50257 fp32 in 4
-// shards, 1500 tokens: 32 us.
+// fewer workgroups share a CU (of 2048 units two, in bf16 by their tables, in
+// fp32 by their registers; of 1024 four in bf16, by their tables, and five in
+// fp32).  A row's runs follow each other on one XCD, whose L2 then serves the
+// history to all but the first.  Few units have a mark: a wave collects its own
+// from its lanes and adjusts them at once, before the mask, which needs no
+// arithmetic.
+// 512 x 131072 bf16 in 8 shards, masks, 100 biases and histories of 4000 tokens
+// on average (most shorter, some of 30000 and more): 70-75 us, and 80 with one
+// of 50000; 67 with 4000 in every row, 62 without masks and biases, 47 with
+// nothing to mark (5.7 TB/s): what marks cost is the instructions of going over
+// the history and of the units to adjust (570 a wave, 330 without masks and
+// biases), not waiting: asking for the next tokens while these are looked at
+// changed nothing.  For the 75, 82 where a row's runs went to all XCDs and 85
+// with every lane adjusting its own units.  4 rows of 131072, 400 tokens: 5.2
+// us; 333 x 50257 fp32 in 4 shards, 1500 tokens: 32-33 us.
 //
 // Counts are whole numbers and a bias's first entry wins by its place in the
 // list, so results do not depend on the order of the atomics.
@@ -62,9 +64,12 @@ struct Span {
   }
 };
 
-// Tokens that a lane asks for at a time: with four, 24 registers fewer let one
-// more workgroup share a CU, where its table does (333 x 50256 fp32: 32 us for
-// 34; 512 x 65536 bf16, 1000 tokens: 31.5 for 32.8; with 20000 82 for 77).
+// Tokens that a lane asks for at a time.  Four, and 24 registers fewer, let one
+// more workgroup of 1024 fp32 units share a CU (333 x 50256 in 4 shards, ~1500
+// tokens: 34 us for 36).  In bf16 the tables of these leave room for four
+// workgroups either way, and four tokens are fewer instructions where a round
+// of them holds the history (512 x 65536 in 8 shards, 1000 tokens: 31.3 for
+// 32.3; 4000: 39.6 for 38.4; 20000: 82 for 76).
 template <int THREADS, int UNITS>
 constexpr int kAhead = THREADS < 512 && UNITS > 1 ? 4 : 8;
 
@@ -337,19 +342,26 @@ int adjust_t(AdjustArgs a, hipStream_t s) {
 // since a workgroup's lanes without entries and its table keep others out.
 // Long histories want the longest runs, which go over them the least often,
 // and more lanes.  us with runs of 256 units (256 lanes, and 128), 512, 1024 and
-// 2048 (512 lanes), bf16, masks and biases, by shards and tokens (~: on average,
-// most less, some ten times as many):
-//   4 rows of 8 x 16384, 400 tokens           5.4     -   5.5
-//   the same, 20000 tokens                   11.9     -  10.1  13.7  12.2
-//   16 rows of 8 x 16384, ~4000              12.1     -   9.9  13.6  11.3
-//   64 rows of 8 x 4096, ~400 (~20000)        6.9     -   7.5   7.1 (56)  8.6 (35)
-//   480 rows of 8 x 526, none                16.3  12.0  33.2  21.8  39.6
-//   266 rows of 16 x 412, ~5700              38.4  51.6  47.7  43.5  57.5
-//   1024 rows of 5 x 3319, 1000              40.8  31.0  49.6  34.1  58.1
-//   512 rows of 8 x 8192, 1000               57.7  41.7  72.4  31.9  48.3
-//   512 rows of 8 x 16384, none             100.3  68.0   124  51.3  56.6
-//   the same, 4000 (20000)                  140.2 125.1   146  65.1 (135)  65.0 (109)
-//   the same, ~4000                             -   169   174  87.1  80.0
+// 2048 (512 lanes), bf16, masks and 16 biases, calls replayed from a graph, by
+// shards and tokens (~: on average, most less, some ten times as many):
+//   4 rows of 8 x 16384, 400 tokens           5.2   5.1   5.2   6.1   6.3
+//   the same, 20000 tokens                   11.3  19.6   8.5  13.6  10.8
+//   16 rows of 8 x 16384, ~4000              12.0  19.7   8.6  13.5  11.0
+//   64 rows of 8 x 4096, ~400                 7.5   7.5   6.8   6.7   7.9
+//   the same, ~20000                         57.5   115  34.0  61.8  35.3
+//   480 rows of 8 x 526, none                12.4   9.1  27.4  17.5  32.9
+//   266 rows of 16 x 412, ~5700              39.5  64.5  47.1  44.2  56.4
+//   1024 rows of 5 x 3319, 1000              40.7  28.3  49.7  33.3  58.8
+//   512 rows of 8 x 8192, 1000               58.2  34.9  72.7  31.2  48.6
+//   512 rows of 8 x 16384, none              82.3  49.4   104  49.7  54.0
+//   the same, 4000                            141   108   147  71.7  67.0
+//   the same, 20000                           358   329   283   149   110
+//   the same, ~4000                           178   158   175  93.8  80.2
+//   512 rows of 8 x 18992, ~4000              208   171   206   111   132
+// The rule's choice is the least of a line or within a seventh of it, but where
+// shards are somewhat longer than a run (3319 and 18992 entries: 33.3 and 132).
+// The histories' lengths are on the device: the rule looks at the size of the
+// list that holds them.
 constexpr uint64_t kFewRuns = 512, kManyRuns = 1024, kLongHistory = 2000;
 
 template <int DT>

@@ -625,7 +625,11 @@ coll_status_t coll_vocab_logprob_backward(const void* const* logits, const int64
  *               ntokens < 2^31; what lies outside is not read).  Its first
  *               prompt[r] tokens (int64 [rows]; 0 without) are the prompt's,
  *               the others the answer's.  A token outside the vocabulary is
- *               padding.
+ *               padding.  ntokens over rows is also taken for the histories'
+ *               length when a kernel is chosen: given a buffer of 2000 and more
+ *               a row for short histories, results are the same, and the call
+ *               up to a fifth slower (twice, where shards have a few hundred
+ *               entries).
  *   repetition, presence, frequency   fp32 [rows]: with c_j the number of
  *               times that token j is among the answer's,
  *                 z_j > 0 ? z_j / repetition : z_j repetition   where the
